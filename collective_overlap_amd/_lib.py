@@ -13,7 +13,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcce.so")
 
 CCE_OK, CCE_EINVAL, CCE_EUNSUPPORTED, CCE_EWORKSPACE, CCE_EHIP = range(5)
-CCE_F32, CCE_BF16 = 0, 1
+CCE_F32, CCE_BF16, CCE_E4M3 = 0, 1, 2
 CCE_MAX_RANKS = 64
 CCE_FLAG_SERIAL = 0x1
 CCE_FLAG_GELU = 0x2
@@ -98,6 +98,20 @@ PROTOTYPES = {
     "cce_overlap_choose": (_I, [ctypes.c_double] * 5),
     "cce_describe_plan": (_I, [_I, _I, _I, _I, _U32, ctypes.c_char_p, _SZ, ctypes.POINTER(_SZ)]),
     "cce_debug_fail_op": (_I, [_I]),
+    "cce_rmsnorm": (_I, [_P, _I, _P, cce_mat, _P, _I64, _P, _I64, _P, _I, ctypes.c_double, _P, _I,
+                         _I64, _P, _I64, _U32, _P]),
+    "cce_rmsnorm_backward_workspace": (_I, [cce_mat, ctypes.POINTER(_SZ)]),
+    "cce_rmsnorm_backward": (_I, [_P, _I, _P, cce_mat, _P, _I, _P, _I64, _P, _I64, ctypes.c_double,
+                                  _P, _I64, _P, _P, _SZ, _U32, _P]),
+    "cce_quantize_blocks": (_I, [_P, _I, _P, cce_mat, _I, _P, _I64, _P, _I64, _U32, _P]),
+    "cce_block_scaled_gemm": (_I, [_P, _I, _P, cce_mat, _P, _I64, _P, cce_mat, _P, _I64, _P,
+                                   cce_mat, _U32, _P]),
+    "cce_ragged_gemm": (_I, [_P, _I, _I, _P, _P, cce_mat, _P, cce_mat, _I64, _P, cce_mat, _U32,
+                             _P]),
+    "cce_ragged_gemm_dgrad": (_I, [_P, _I, _I, _P, _P, cce_mat, _P, cce_mat, _I64, _P, cce_mat,
+                                   _U32, _P]),
+    "cce_ragged_gemm_wgrad": (_I, [_P, _I, _I, _P, _P, cce_mat, _P, cce_mat, _P, cce_mat, _I64,
+                                   _U32, _P]),
 }
 
 

@@ -16,7 +16,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (CCE_BF16, CCE_F32, CCE_FLAG_BIDIRECTIONAL, CCE_FLAG_COPY_DMA,
+from ._lib import (CCE_BF16, CCE_E4M3, CCE_F32, CCE_FLAG_BIDIRECTIONAL, CCE_FLAG_COPY_DMA,
                    CCE_FLAG_FINE_GRAINED, CCE_FLAG_FUSED_PERMUTE, CCE_FLAG_GELU,
                    CCE_FLAG_ONE_CHAIN, CCE_FLAG_SERIAL,
                    AG_MODES, RS_MODES,
@@ -30,6 +30,9 @@ __all__ = [
     "cce_fused_reduce_epilogue", "cce_fused_reduce_epilogue_batched",
     "cce_fused_allreduce_epilogue", "cce_describe_plan", "cce_debug_fail_op",
     "cce_debug_signal_giveup", "cce_version",
+    "cce_rmsnorm", "cce_rmsnorm_backward", "cce_rmsnorm_backward_workspace",
+    "cce_quantize_blocks", "cce_block_scaled_gemm",
+    "cce_ragged_gemm", "cce_ragged_gemm_dgrad", "cce_ragged_gemm_wgrad",
     "CCE_FLAG_SERIAL", "CCE_FLAG_GELU", "CCE_FLAG_COPY_DMA", "CCE_FLAG_FUSED_PERMUTE",
     "CCE_FLAG_BIDIRECTIONAL", "CCE_FLAG_FINE_GRAINED", "CCE_FLAG_ONE_CHAIN",
     "AG_MODES", "RS_MODES",
@@ -121,7 +124,7 @@ class Context:
         n = ctypes.c_int()
         check(lib().cce_ctx_read_profile(self._h, max_records, recs, ctypes.byref(n)),
               "cce_ctx_read_profile")
-        kinds = {0: "gemm", 1: "copy", 2: "epilogue"}
+        kinds = {0: "gemm", 1: "copy", 2: "epilogue", 4: "norm", 5: "quantize"}
         return [dict(kind=kinds.get(r.kind, str(r.kind)), iter=r.iter, ms=r.ms, flops=r.flops,
                      bytes=r.bytes) for r in recs[:n.value]]
 
@@ -461,3 +464,178 @@ def cce_fused_allreduce_epilogue(ctx: Context, partials, bias, residual, outs, p
         mask_out.data_ptr() if mask_out is not None else None, 0,
         _stream(stream, outs[0].device)), "cce_fused_allreduce_epilogue")
     return outs
+
+
+# ---- operators around the einsums ---------------------------------------------
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _shape_is(t, shape, what):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _vector(t, n, what):
+    _shape_is(t, (n,), what)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _scales(t, rows, cols, block_rows, what):
+    """E8M0 scales of a [rows, cols] matrix in block_rows x 128 blocks."""
+    _dtype_is([t], _E8M0, what)
+    _shape_is(t, (-(-rows // block_rows), -(-cols // 128)), what)
+    return _mat(t)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def cce_rmsnorm(ctx: Context, x, weight, out, eps: float = 1e-5, residual=None, residual_out=None,
+                scales=None, stream=None):
+    """r = x + residual (rounded to x's dtype); out = r / sqrt(mean(r^2) + eps) * weight, row by
+    row.  out: float32, bfloat16, or float8_e4m3fn with scales (float8_e8m0fnu, one per row and
+    128 columns).  residual_out, if given, receives r."""
+    xm, om = _mat(x), _mat(out)
+    same = [t for t in (residual, residual_out) if t is not None]
+    _dtype_is(same, x.dtype, "the residual")
+    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (out, "out")):
+        if t is not None:
+            _shape_is(t, x.shape, what)
+    _vector(weight, xm.cols, "weight")
+    quantized = out.dtype == _E4M3
+    if quantized != (scales is not None):
+        raise ValueError("scales go with a float8_e4m3fn output")
+    sm = _scales(scales, xm.rows, xm.cols, 1, "scales") if quantized else cce_mat(0, 0, 0)
+    rm = _mat(residual) if residual is not None else xm
+    rom = _mat(residual_out) if residual_out is not None else xm
+    _on_device(ctx, [x, weight, out, residual, residual_out, scales])
+    check(lib().cce_rmsnorm(
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, _ptr(residual), rm.ld, _ptr(residual_out),
+        rom.ld, weight.data_ptr(), _dtype(weight.dtype), float(eps), out.data_ptr(),
+        CCE_E4M3 if quantized else _dtype(out.dtype), om.ld, _ptr(scales), sm.ld, 0,
+        _stream(stream, out.device)), "cce_rmsnorm")
+    return out
+
+
+def cce_rmsnorm_backward_workspace(shape) -> int:
+    """shape: (rows, cols)."""
+    nb = ctypes.c_size_t()
+    check(lib().cce_rmsnorm_backward_workspace(cce_mat(shape[0], shape[1], -(-shape[1] // 8) * 8),
+                                               ctypes.byref(nb)), "cce_rmsnorm_backward_workspace")
+    return nb.value
+
+
+def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: float = 1e-5,
+                         d_residual=None, workspace=None, stream=None):
+    """Gradients of cce_rmsnorm for its normalised tensor x (residual_out where a residual was
+    added): dx, of both summands, with d_residual added; dweight (float32), if given."""
+    xm = _mat(x)
+    _dtype_is([dout, dx, d_residual], x.dtype, "dout, dx and d_residual")
+    for t, what in ((dout, "dout"), (dx, "dx"), (d_residual, "d_residual")):
+        if t is not None:
+            _shape_is(t, x.shape, what)
+    _vector(weight, xm.cols, "weight")
+    if dweight is not None:
+        _dtype_is([dweight], torch.float32, "dweight")
+        _vector(dweight, xm.cols, "dweight")
+    _on_device(ctx, [x, weight, dout, dx, dweight, d_residual, workspace])
+    rm = _mat(d_residual) if d_residual is not None else xm
+    ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(x.shape), dx.device, workspace,
+                         stream)
+    check(lib().cce_rmsnorm_backward(
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, weight.data_ptr(), _dtype(weight.dtype),
+        dout.data_ptr(), _mat(dout).ld, _ptr(d_residual), rm.ld, float(eps), dx.data_ptr(),
+        _mat(dx).ld, _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
+        "cce_rmsnorm_backward")
+    return dx
+
+
+def cce_quantize_blocks(ctx: Context, x, q, scales, block_rows: int = 1, stream=None):
+    """q (float8_e4m3fn) and scales (float8_e8m0fnu) of x in blocks of block_rows x 128:
+    block_rows 1 for left operands, 128 for right operands of cce_block_scaled_gemm."""
+    xm, qm = _mat(x), _mat(q)
+    _dtype_is([q], _E4M3, "q")
+    _shape_is(q, x.shape, "q")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    sm = _scales(scales, xm.rows, xm.cols, block_rows, "scales")
+    _on_device(ctx, [x, q, scales])
+    check(lib().cce_quantize_blocks(
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, block_rows, q.data_ptr(), qm.ld,
+        scales.data_ptr(), sm.ld, 0, _stream(stream, q.device)), "cce_quantize_blocks")
+    return q
+
+
+def cce_block_scaled_gemm(ctx: Context, a, a_scales, b, b_scales, c, gelu: bool = False,
+                          stream=None):
+    """c = a @ b^T over float8_e4m3fn operands: a [M, K] with a scale per row and 128 columns,
+    b [N, K] with a scale per 128 x 128 block."""
+    am, bm, cm = _mat(a), _mat(b), _mat(c)
+    _dtype_is([a, b], _E4M3, "a and b")
+    sam = _scales(a_scales, am.rows, am.cols, 1, "a_scales")
+    sbm = _scales(b_scales, bm.rows, bm.cols, 128, "b_scales")
+    _on_device(ctx, [a, a_scales, b, b_scales, c])
+    check(lib().cce_block_scaled_gemm(
+        ctx.handle, _dtype(c.dtype), a.data_ptr(), am, a_scales.data_ptr(), sam.ld, b.data_ptr(),
+        bm, b_scales.data_ptr(), sbm.ld, c.data_ptr(), cm, CCE_FLAG_GELU if gelu else 0,
+        _stream(stream, c.device)), "cce_block_scaled_gemm")
+    return c
+
+
+def _experts(b, what):
+    """[experts, N, K] as one expert's matrix and the elements from one to the next."""
+    if b.dim() != 3 or b.shape[0] < 1:
+        raise ValueError(f"{what} must be [experts, N, K]")
+    return _mat(b[0]), (b.stride(0) if b.shape[0] > 1 else 0)
+
+
+def _offsets(offsets, experts):
+    _dtype_is([offsets], torch.int64, "offsets")
+    _vector(offsets, experts + 1, "offsets")
+
+
+def cce_ragged_gemm(ctx: Context, a, b, offsets, c, stream=None):
+    """c[r] = a[r] @ b[e]^T for the rows r in [offsets[e], offsets[e + 1]) of every expert e.
+    a [T, K] and b [experts, N, K] bfloat16, c [T, N], offsets int64 on the device; rows that
+    belong to no expert are left as they were."""
+    am, cm = _mat(a), _mat(c)
+    bm, stride = _experts(b, "b")
+    _dtype_is([a, b], torch.bfloat16, "a and b")
+    _offsets(offsets, b.shape[0])
+    _on_device(ctx, [a, b, offsets, c])
+    check(lib().cce_ragged_gemm(
+        ctx.handle, _dtype(c.dtype), b.shape[0], offsets.data_ptr(), a.data_ptr(), am,
+        b.data_ptr(), bm, stride, c.data_ptr(), cm, 0, _stream(stream, c.device)),
+        "cce_ragged_gemm")
+    return c
+
+
+def cce_ragged_gemm_dgrad(ctx: Context, dc, b, offsets, da, stream=None):
+    """Gradient of cce_ragged_gemm's rows: da[r] = dc[r] @ b[e]."""
+    cm, am = _mat(dc), _mat(da)
+    bm, stride = _experts(b, "b")
+    _dtype_is([dc, b], torch.bfloat16, "dc and b")
+    _offsets(offsets, b.shape[0])
+    _on_device(ctx, [dc, b, offsets, da])
+    check(lib().cce_ragged_gemm_dgrad(
+        ctx.handle, _dtype(da.dtype), b.shape[0], offsets.data_ptr(), dc.data_ptr(), cm,
+        b.data_ptr(), bm, stride, da.data_ptr(), am, 0, _stream(stream, da.device)),
+        "cce_ragged_gemm_dgrad")
+    return da
+
+
+def cce_ragged_gemm_wgrad(ctx: Context, dc, a, offsets, db, stream=None):
+    """Gradient of cce_ragged_gemm's weights: db[e] = dc[rows of e]^T @ a[rows of e], zero for
+    an expert without rows."""
+    cm, am = _mat(dc), _mat(a)
+    bm, stride = _experts(db, "db")
+    _dtype_is([dc, a], torch.bfloat16, "dc and a")
+    _offsets(offsets, db.shape[0])
+    _on_device(ctx, [dc, a, offsets, db])
+    check(lib().cce_ragged_gemm_wgrad(
+        ctx.handle, _dtype(db.dtype), db.shape[0], offsets.data_ptr(), dc.data_ptr(), cm,
+        a.data_ptr(), am, db.data_ptr(), bm, stride, 0, _stream(stream, db.device)),
+        "cce_ragged_gemm_wgrad")
+    return db

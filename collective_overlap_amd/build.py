@@ -24,7 +24,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcce.so")
 ROOT = os.path.dirname(PKG)
 
-SOURCES = ["gemm.hip", "epilogue.hip", "permute.hip", "plan.cpp", "abi.cpp"]
+SOURCES = ["gemm.hip", "epilogue.hip", "permute.hip", "norm.hip", "gemm8.hip", "ragged.hip",
+           "plan.cpp", "abi.cpp", "layer.cpp"]
 # Standalone measurement programs, not part of the library: the rate the
 # matrix cores sustain on MFMAs and LDS operand reads alone (bench.py
 # --mfma-ceiling runs it), and what HBM sustains for plain streaming kernels

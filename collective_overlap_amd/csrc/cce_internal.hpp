@@ -147,6 +147,80 @@ struct EpilogueLaunch {
 cce_status launch_fused_epilogue(const EpilogueLaunch& e, void* stream);
 
 // ---------------------------------------------------------------------------
+// Operators around the einsums (layer.cpp validates, the kernels are in
+// norm.hip, gemm8.hip and ragged.hip).  Extents are positive and every stride
+// and pointer already checked.
+// ---------------------------------------------------------------------------
+struct NormLaunch {
+  cce_dtype x_t = CCE_BF16, w_t = CCE_BF16, out_t = CCE_BF16;
+  const void* x = nullptr;
+  const void* res = nullptr;      // NULL: none
+  void* res_out = nullptr;        // NULL: not wanted
+  const void* w = nullptr;
+  void* out = nullptr;
+  uint8_t* scales = nullptr;      // out_t CCE_E4M3
+  int64_t rows = 0, cols = 0, ld_x = 0, ld_res = 0, ld_res_out = 0, ld_out = 0, ld_scales = 0;
+  float eps = 0;
+};
+cce_status launch_rmsnorm(const NormLaunch& L, void* stream);
+
+struct NormBackwardLaunch {
+  cce_dtype x_t = CCE_BF16, w_t = CCE_BF16;
+  const void* x = nullptr;
+  const void* w = nullptr;
+  const void* dout = nullptr;
+  const void* dres = nullptr;     // NULL: none
+  void* dx = nullptr;
+  float* dw = nullptr;            // NULL: not wanted
+  void* workspace = nullptr;      // rmsnorm_backward_bytes
+  int64_t rows = 0, cols = 0, ld_x = 0, ld_dout = 0, ld_dres = 0, ld_dx = 0;   // rows may be 0: dw = 0
+  float eps = 0;
+};
+size_t rmsnorm_backward_bytes(int64_t rows, int64_t cols);
+cce_status launch_rmsnorm_backward(const NormBackwardLaunch& L, void* stream);
+
+struct QuantizeLaunch {
+  cce_dtype x_t = CCE_BF16;
+  const void* x = nullptr;
+  uint8_t* q = nullptr;
+  uint8_t* scales = nullptr;
+  int block_rows = 1;             // 1 or 128
+  int64_t rows = 0, cols = 0, ld_x = 0, ld_q = 0, ld_scales = 0;
+};
+cce_status launch_quantize_blocks(const QuantizeLaunch& L, void* stream);
+
+struct Gemm8Launch {
+  const uint8_t* a = nullptr;
+  const uint8_t* b = nullptr;
+  const uint8_t* sa = nullptr;    // [M, ceil(K / 128)]
+  const uint8_t* sb = nullptr;    // [ceil(N / 128), ceil(K / 128)]
+  void* c = nullptr;
+  cce_dtype out_t = CCE_BF16;
+  bool gelu = false;
+  int64_t M = 0, N = 0, K = 0, lda = 0, ldb = 0, ldc = 0, ld_sa = 0, ld_sb = 0;   // K may be 0
+};
+cce_status launch_gemm8(const Gemm8Launch& L, void* stream);
+
+// Products of rows grouped by expert: rows [offsets[e], offsets[e + 1]) of the
+// row operands belong to expert e.
+enum RaggedKind : int {
+  RAGGED_FORWARD = 0,   // c[r, n] = sum_k a[r, k] b_e[n, k]
+  RAGGED_DGRAD = 1,     // a[r, k] = sum_n c[r, n] b_e[n, k]
+  RAGGED_WGRAD = 2,     // b_e[n, k] = sum_r c[r, n] a[r, k]
+};
+struct RaggedLaunch {
+  int kind = RAGGED_FORWARD;
+  int experts = 0;
+  const int64_t* offsets = nullptr;
+  void* a = nullptr;              // [T, K]
+  void* b = nullptr;              // [experts][N, K]
+  void* c = nullptr;              // [T, N]
+  cce_dtype out_t = CCE_BF16;     // of the result; the other two are bf16
+  int64_t T = 0, N = 0, K = 0, lda = 0, ldb = 0, ldc = 0, stride_b = 0;
+};
+cce_status launch_ragged(const RaggedLaunch& L, void* stream);
+
+// ---------------------------------------------------------------------------
 // Plan IR: the ordered operations of one looped call, independent of HIP.
 // Buffers are symbolic so that the same plan can be printed and race-checked
 // on the host, and resolved to device pointers by the executor.
