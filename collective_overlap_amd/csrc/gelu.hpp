@@ -1,4 +1,5 @@
-// GELU as the products' epilogues apply it (gemm.hip, gemm8.hip).
+// GELU as the 8-bit product applies it (gemm8.hip): the same arithmetic as the
+// grouped GEMM's epilogue (gemm.hip), so that both give the same bits.
 #pragma once
 
 #include <hip/hip_runtime.h>
