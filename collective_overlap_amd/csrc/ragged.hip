@@ -5,14 +5,38 @@
 //   dgrad    A[r, k]   = sum_n C[r, n] B_e[n, k]
 //   wgrad    B_e[n, k] = sum over the expert's rows r of C[r, n] A[r, k]
 //
-// bf16 operands, fp32 accumulation.  The offsets are read on the device, so
-// the host needs no count of any expert's rows.
+// One kernel computes all three as Z[i, j] = sum_l X[i, l] Y[j, l] per expert,
+// in bf16 with fp32 accumulation (v_mfma_f32_32x32x16_bf16).  An operand is
+// stored either with l contiguous ("row" form: A, and B in the forward
+// product) or with i or j contiguous ("column" form: B in dgrad, both
+// operands in wgrad); nothing is transposed in memory.
+//
+// Staging.  Tiles of 64 l go from global memory to LDS directly (16 bytes per
+// lane), two stages, as the grouped GEMM does it (gemm.hip): the loads of a
+// stage are spread over the matrix instructions of the one before.
+//   row form: LDS rows of 64 l (128 bytes), 16-byte chunks XOR-swizzled by the
+//     row so that 32 rows read at one chunk spread over the banks; a lane's
+//     fragment (8 consecutive l of one row) is one 16-byte read.
+//   column form: LDS rows of one l (BM or BN elements).  A fragment is two
+//     transposing reads (ds_read_b64_tr_b16): 16 lanes read 4 l x 16 columns
+//     and each gets 4 l of its own column.  Chunk c of row l is kept at
+//     c ^ ((l & 3) << 2), so that the 4 rows that 32 lanes read at 64 bytes
+//     each fall on all 64 banks.
+// Where l ends: chunks and rows past the end are out of the buffer's range
+// and land as zeros; a last chunk that is partly past the end (row form, l
+// not a multiple of 8) is zeroed in LDS, since what lies behind a row may be
+// anything, NaN included.
+//
+// The offsets are read on the device: every workgroup finds its tile from
+// them (a scan over the experts), so the host needs no count of any expert's
+// rows and launches the most tiles there can be.
 
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "cce_internal.hpp"
 
@@ -20,91 +44,459 @@ namespace cce {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-// One product per expert, X[i, l] Y[j, l] summed over l, with any strides.
+constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
+constexpr uint32_t kOob = 0x40000000;      // past every buffer below
+constexpr int kBL = 64;                    // l per tile
+constexpr int kNW = 4;                     // waves
+
 struct RArgs {
   const __bf16* x;
   const __bf16* y;
   void* z;
   const int64_t* offsets;
-  int64_t T;
+  int T;
   int experts, I, J, L;       // extents that do not depend on the expert
-  int64_t xi, xl, xe;         // strides of X along i, l and from expert to expert
-  int64_t yj, yl, ye;
-  int64_t zi, ze;             // strides of the result along i and from expert to expert
+  int ldx, ldy, ldz;
+  int64_t xe, ye, ze;         // strides from expert to expert
   int tiles_j;
-  bool rows_i;                // the expert's rows are i (forward, dgrad) or l (wgrad)
 };
 
-// The next row number of the offsets: kept within [0, T] and not below the one
-// before, so that no access leaves the operands and no row has two experts,
-// whatever the offsets hold.
-__device__ __forceinline__ int64_t next_row(const int64_t* offsets, int e, int64_t T, int64_t before) {
-  return min(max(offsets[e], before), T);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const int n = bytes <= 0 ? 0 : static_cast<int>(min((bytes + 15) & ~int64_t{15}, static_cast<int64_t>(kOob) - 256));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
 }
 
-template <typename TOut>
-__global__ __launch_bounds__(256) void ragged_kernel(RArgs a) {
-  constexpr int B = 64, BL = 32, ROW = BL + 8;
-  __shared__ __attribute__((aligned(16))) __bf16 shx[B * ROW];
-  __shared__ __attribute__((aligned(16))) __bf16 shy[B * ROW];
-  int t = blockIdx.x / a.tiles_j;
-  const int tj = blockIdx.x - t * a.tiles_j;
-  int e = 0;
-  int64_t lo = 0, hi = 0;
-  if (a.rows_i) {
-    hi = next_row(a.offsets, 0, a.T, 0);
-    for (;; ++e) {
-      if (e == a.experts) return;
-      lo = hi;
-      hi = next_row(a.offsets, e + 1, a.T, lo);
-      const int tiles = static_cast<int>((hi - lo + B - 1) / B);
-      if (t < tiles) break;
-      t -= tiles;
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voffset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, voffset, 0, 0, 0);
+}
+
+// s_waitcnt vmcnt(0), the other counters left alone.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Row number i of the offsets, within [0, T].  (Callers take the running
+// maximum, so that no row has two experts, whatever the offsets hold.)
+__device__ __forceinline__ int row_number(const RArgs& a, int i) {
+  const int64_t v = a.offsets[i];
+  return v < 0 ? 0 : v > a.T ? a.T : static_cast<int>(v);
+}
+
+__device__ __forceinline__ int wave_max(int v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = max(v, __shfl_xor(v, m));
+  return v;
+}
+
+struct Tile {
+  int e, lo, hi;    // expert and its rows
+  int ti, tj;
+};
+
+// Tile rows of a tile height, from the experts' rows: calls f(first tile row,
+// tile rows, expert, lo, hi) for the lane's expert of every group of 64.
+// Returns the number of all tile rows.
+template <int BM, typename F>
+__device__ __forceinline__ int scan_experts(const RArgs& a, F&& f) {
+  const int lane = threadIdx.x & 63;
+  int before = row_number(a, 0), rows = 0;     // end of the rows, tile rows so far
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    const int e = e0 + lane;
+    int hi = max(row_number(a, min(e, a.experts - 1) + 1), before);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(hi, d);
+      if (lane >= d) hi = max(hi, o);
     }
+    const int prev = __shfl_up(hi, 1);
+    const int lo = lane == 0 ? before : prev;
+    const int mine = e < a.experts ? (hi - lo + BM - 1) / BM : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(sum, d);
+      if (lane >= d) sum += o;
+    }
+    f(rows + sum - mine, mine, e, lo, hi);
+    rows += __shfl(sum, 63);
+    before = __shfl(hi, 63);
+  }
+  return rows;
+}
+
+// Tiles of the expert's rows (forward, dgrad).  Workgroups are dealt to the 8
+// XCDs in turn: each XCD gets a contiguous range of the tiles there are, and
+// walks an expert's tiles in bands of 4 tile rows, so that the tiles in
+// flight share X and Y in the XCD's L2.  false: no tile for this workgroup.
+template <int BM>
+__device__ __forceinline__ bool find_row_tile(const RArgs& a, Tile& t) {
+  const int rows = __builtin_amdgcn_readfirstlane(scan_experts<BM>(a, [](int, int, int, int, int) {}));
+  const int64_t tiles = static_cast<int64_t>(rows) * a.tiles_j;
+  const int64_t per = (tiles + 7) / 8;
+  const int w = blockIdx.x;
+  const int64_t id = (w & 7) * per + (w >> 3);
+  if ((w >> 3) >= per || id >= tiles) return false;
+  int first = 0, mine = 0, e = 0, lo = 0, hi = 0;
+  scan_experts<BM>(a, [&](int f, int n, int ex, int l, int h) {
+    const uint64_t found = __ballot(n > 0 && static_cast<int64_t>(f) * a.tiles_j <= id &&
+                                    id < static_cast<int64_t>(f + n) * a.tiles_j);
+    if (found) {
+      const int src = __ffsll(static_cast<unsigned long long>(found)) - 1;
+      first = __shfl(f, src);
+      mine = __shfl(n, src);
+      e = __shfl(ex, src);
+      lo = __shfl(l, src);
+      hi = __shfl(h, src);
+    }
+  });
+  t.e = __builtin_amdgcn_readfirstlane(e);
+  t.lo = __builtin_amdgcn_readfirstlane(lo);
+  t.hi = __builtin_amdgcn_readfirstlane(hi);
+  const int rem = static_cast<int>(id - static_cast<int64_t>(first) * a.tiles_j);
+  constexpr int kBand = 4;
+  const int band = rem / (kBand * a.tiles_j);
+  const int in_band = rem - band * kBand * a.tiles_j;
+  const int height = min(mine - band * kBand, kBand);
+  t.ti = __builtin_amdgcn_readfirstlane(band * kBand + in_band % height);
+  t.tj = __builtin_amdgcn_readfirstlane(in_band / height);
+  return true;
+}
+
+// Tiles of every expert's matrix (wgrad), in the same order.
+template <int BM>
+__device__ __forceinline__ void find_matrix_tile(const RArgs& a, Tile& t) {
+  const int w = blockIdx.x, per = gridDim.x / 8;
+  const int id = w < per * 8 ? (w & 7) * per + (w >> 3) : w;
+  const int tiles_i = (a.I + BM - 1) / BM;
+  t.e = id / (tiles_i * a.tiles_j);
+  const int rem = id - t.e * tiles_i * a.tiles_j;
+  constexpr int kBand = 4;
+  const int band = rem / (kBand * a.tiles_j);
+  const int in_band = rem - band * kBand * a.tiles_j;
+  const int height = min(tiles_i - band * kBand, kBand);
+  t.ti = band * kBand + in_band % height;
+  t.tj = in_band / height;
+  int lo = 0;
+  for (int i = threadIdx.x & 63; i <= t.e; i += 64) lo = max(lo, row_number(a, i));
+  lo = wave_max(lo);
+  t.lo = __builtin_amdgcn_readfirstlane(lo);
+  t.hi = __builtin_amdgcn_readfirstlane(max(lo, row_number(a, t.e + 1)));
+}
+
+// A transposing read.  (The restrict pointer gives it alias information, as an
+// ordinary load has by its type; without any the compiler takes it to depend
+// on every load to LDS in flight and waits for them, 8 times a tile.)
+__device__ __forceinline__ s16x4 tr_read(const __attribute__((address_space(3))) s16x4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s16x4>(p));
+}
+
+// One operand's share of a tile: its loads and its fragments.  BT: rows of
+// the tile (i or j); WT: rows of a wave; COL: the column form.
+template <int BT, int WT, bool COL>
+struct Operand {
+  static constexpr int kChunks = COL ? BT / 8 : kBL / 8;      // 16-byte chunks per LDS row
+  static constexpr int kRowBytes = kChunks * 16;
+  static constexpr int kBytes = BT * kBL * 2;
+  static constexpr int kRPI = 64 / kChunks;                   // LDS rows per load instruction
+  static constexpr int kLoads = kBytes / (1024 * kNW);        // load instructions per wave
+  static constexpr int kFrags = WT / 32;
+  static_assert(!COL || kChunks >= 16, "the swizzle needs 16 chunks");
+
+  const __bf16* base;      // (tile's first row, l = 0)
+  int ld, rows, L;
+  uint32_t off[kLoads];
+  int chunk;               // of the lane's loads, row form
+  int f0, fsw[4], ftr[4];  // fragment addresses
+
+  __device__ __forceinline__ void init(const __bf16* b, int ld_, int rows_, int L_, int lane, int wave, int wt) {
+    base = b;
+    ld = ld_;
+    rows = rows_;
+    L = L_;
+    const int r0 = lane / kChunks, c = lane % kChunks;
+    chunk = COL ? 0 : c ^ swz(kRPI * wave + r0);    // (the swizzle of rows kRPI * kNW * p further is the same)
+#pragma unroll
+    for (int p = 0; p < kLoads; ++p) {
+      const int r = kRPI * (kNW * p + wave) + r0;   // LDS row: i, or l
+      off[p] = static_cast<uint32_t>(r) * ld * 2u + 16u * (COL ? c ^ ((r & 3) << 2) : chunk);
+    }
+    const int h = lane >> 5;
+    if constexpr (COL) {
+      // lane q of a group of 16 reads row q / 4, columns 4 (q % 4) .. + 3
+      const int q = lane & 15, m = q >> 2;
+      const int byte = 2 * (16 * ((lane >> 4) & 1) + 4 * (q & 3));       // in the wave's 32 columns
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) {
+        const int cc = (wt * WT + 32 * f) / 8 + (byte >> 4);
+        ftr[f] = (8 * h + m) * kRowBytes + ((cc ^ (m << 2)) << 4) + (byte & 15);
+      }
+    } else {
+      const int r = lane & 31;
+      f0 = (wt * WT + r) * kRowBytes;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) fsw[kk] = ((2 * kk + h) ^ swz(r)) << 4;
+    }
+  }
+
+  // Buffer of the tile at l0: rows past the end are out of its range.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int l0) const {
+    if constexpr (COL) {
+      const int n = min(L - l0, kBL);
+      return make_rsrc(base + static_cast<int64_t>(l0) * ld,
+                       n <= 0 ? 0 : (static_cast<int64_t>(n - 1) * ld + rows) * 2);
+    } else {
+      return make_rsrc(base, (static_cast<int64_t>(min(rows, BT) - 1) * ld + L) * 2);
+    }
+  }
+  // What the tile at l0 adds to the lane's offsets.
+  __device__ __forceinline__ uint32_t add(int l0) const {
+    return COL ? 0u : l0 * 2u + (l0 + chunk * 8 < L ? 0u : kOob);
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t add, int p, int wave) const {
+    dma16(r, lds + (p * kNW + wave) * 1024, off[p] + add);
+  }
+  // Fragment f of l step kk (16 l): 8 l of the lane's row.
+  __device__ __forceinline__ bf16x8 frag(const char* lds, int kk, int f) const {
+    if constexpr (COL) {
+      const char* p = lds + ftr[f] + kk * 16 * kRowBytes;
+      const s16x4 lo = tr_read((lds_s16x4)(p));
+      const s16x4 hi = tr_read((lds_s16x4)(p + 4 * kRowBytes));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lds + f0 + fsw[kk] + f * 32 * kRowBytes));
+    }
+  }
+  // Zeroes what a last chunk holds past the end of l (row form).
+  __device__ __forceinline__ void zero_tail(char* lds, int l0) const {
+    if constexpr (!COL) {
+      const int l = L - l0;                      // in the tile: 0 < l < 64, l % 8 != 0
+      for (int r = threadIdx.x; r < BT; r += 64 * kNW) {
+        __bf16* c = reinterpret_cast<__bf16*>(lds + r * kRowBytes + (((l >> 3) ^ swz(r)) << 4));
+        for (int e = l & 7; e < 8; ++e) c[e] = static_cast<__bf16>(0.0f);
+      }
+    }
+  }
+};
+
+template <int BM, int BN, bool XC, bool YC, typename TOut>
+__global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
+  constexpr int WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
+  using OX = Operand<BM, WTM, XC>;
+  using OY = Operand<BN, WTN, YC>;
+  constexpr int STAGE = OX::kBytes + OY::kBytes;
+  constexpr int N_DMA = OX::kLoads + OY::kLoads;
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+
+  Tile t;
+  if constexpr (XC) {
+    find_matrix_tile<BM>(a, t);
   } else {
-    const int tiles_i = (a.I + B - 1) / B;
-    e = t / tiles_i;
-    t -= e * tiles_i;
-    for (int i = 0; i <= e; ++i) lo = next_row(a.offsets, i, a.T, lo);
-    hi = next_row(a.offsets, e + 1, a.T, lo);
+    if (!find_row_tile<BM>(a, t)) return;
   }
-  const int64_t I = a.rows_i ? hi - lo : a.I;
-  const int64_t L = a.rows_i ? a.L : hi - lo;
-  const __bf16* x = a.x + e * a.xe + (a.rows_i ? lo * a.xi : lo * a.xl);
-  const __bf16* y = a.y + e * a.ye + (a.rows_i ? 0 : lo * a.yl);
-  TOut* z = reinterpret_cast<TOut*>(a.z) + e * a.ze + (a.rows_i ? lo * a.zi : 0);
-  const int64_t i0 = static_cast<int64_t>(t) * B;
-  const int j0 = tj * B;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
-  const int r = lane & 31, h = lane >> 5;
-  f32x16 acc = {};
-  for (int64_t l0 = 0; l0 < L; l0 += BL) {
+  const int i0 = t.ti * BM, j0 = t.tj * BN;
+  const int I = XC ? a.I : t.hi - t.lo, L = XC ? t.hi - t.lo : a.L;
+  const __bf16* x = a.x + t.e * a.xe + (XC ? static_cast<int64_t>(t.lo) * a.ldx + i0
+                                           : static_cast<int64_t>(t.lo + i0) * a.ldx);
+  const __bf16* y = a.y + t.e * a.ye + (YC ? static_cast<int64_t>(XC ? t.lo : 0) * a.ldy + j0
+                                           : static_cast<int64_t>(j0) * a.ldy);
+  TOut* z = reinterpret_cast<TOut*>(a.z) + t.e * a.ze + (XC ? 0 : static_cast<int64_t>(t.lo) * a.ldz);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  OX ox;
+  OY oy;
+  ox.init(x, a.ldx, I - i0, L, lane, wave, wm);
+  oy.init(y, a.ldy, a.J - j0, L, lane, wave, wn);
+
+  bf16x8 fx[2][FM], fy[2][FN];
+  auto fread = [&](int buf, int kk, int slot, int q) {
+    const char* s = smem + buf * STAGE;
+    if (q < FN) fy[slot][q] = oy.frag(s + OX::kBytes, kk, q);
+    else fx[slot][q - FN] = ox.frag(s, kk, q - FN);
+  };
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+  // Blocks in a snake order: consecutive instructions share an operand.
+  auto mfma = [&](int slot, int q) {
+    const int i = q / FM, j = (i & 1) ? FM - 1 - q % FM : q % FM;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[slot][i], fx[slot][j], acc[i][j], 0, 0, 0);
+  };
+
+  const int KT = (L + kBL - 1) / kBL;
+  const bool tail = (!XC || !YC) && (L & 7) != 0;
+  auto load_all = [&](int buf, int l0) {
+    const __amdgpu_buffer_rsrc_t rx = ox.rsrc(l0), ry = oy.rsrc(l0);
+    const uint32_t ax = ox.add(l0), ay = oy.add(l0);
+    char* s = smem + buf * STAGE;
+#pragma unroll
+    for (int p = 0; p < OX::kLoads; ++p) ox.load(rx, s, ax, p, wave);
+#pragma unroll
+    for (int p = 0; p < OY::kLoads; ++p) oy.load(ry, s + OX::kBytes, ay, p, wave);
+  };
+  auto mend_tail = [&](int buf, int kt) {
+    if (tail && kt == KT - 1) {
+      char* s = smem + buf * STAGE;
+      ox.zero_tail(s, kt * kBL);
+      oy.zero_tail(s + OX::kBytes, kt * kBL);
+      __syncthreads();
+    }
+  };
+  if (KT > 0) {
+    load_all(0, 0);
+    wait_loads();
     __syncthreads();
-    for (int p = tid; p < B * BL; p += 256) {
-      // consecutive threads along the operand's contiguous dimension
-      const int ix = a.xl == 1 ? p / BL : p % B, lx = a.xl == 1 ? p % BL : p / B;
-      const int iy = a.yl == 1 ? p / BL : p % B, ly = a.yl == 1 ? p % BL : p / B;
-      shx[ix * ROW + lx] = i0 + ix < I && l0 + lx < L ? x[(i0 + ix) * a.xi + (l0 + lx) * a.xl] : __bf16(0.0f);
-      shy[iy * ROW + ly] = j0 + iy < a.J && l0 + ly < L ? y[(j0 + iy) * a.yj + (l0 + ly) * a.yl] : __bf16(0.0f);
+    mend_tail(0, 0);
+#pragma unroll
+    for (int q = 0; q < FM + FN; ++q) fread(0, 0, 0, q);
+    load_all(1, kBL);
+  }
+  // Per tile: steps 0..2 read the next step's fragments between their matrix
+  // instructions; then the next tile's loads are waited for, and the last
+  // step reads its first fragments while the loads of the tile after it go
+  // into this tile's buffer.
+  constexpr int NMF = FM * FN;
+  constexpr int RS = NMF >= 2 * (FM + FN) ? 2 : 1;
+  for (int kt = 0; kt < KT; ++kt) {
+    const int cur = kt & 1, nxt = cur ^ 1;
+#pragma unroll
+    for (int kk = 0; kk < 3; ++kk) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < NMF; ++q) {
+        mfma(kk & 1, q);
+        if (q % RS == 0 && q / RS < FM + FN) fread(cur, kk + 1, (kk + 1) & 1, q / RS);
+        if (NMF < FM + FN && q == NMF - 1) {
+#pragma unroll
+          for (int r = NMF; r < FM + FN; ++r) fread(cur, kk + 1, (kk + 1) & 1, r);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_loads();
+    __syncthreads();
+    mend_tail(nxt, kt + 1);
+    {
+      const int l0 = (kt + 2) * kBL;
+      const __amdgpu_buffer_rsrc_t rx = ox.rsrc(l0), ry = oy.rsrc(l0);
+      const uint32_t ax = ox.add(l0), ay = oy.add(l0);
+      char* s = smem + cur * STAGE;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < NMF; ++q) {
+        mfma(1, q);
+        if (q % RS == 0 && q / RS < FM + FN) fread(nxt, 0, 0, q / RS);
+        if (NMF < FM + FN && q == NMF - 1) {
+#pragma unroll
+          for (int r = NMF; r < FM + FN; ++r) fread(nxt, 0, 0, r);
+        }
+#pragma unroll
+        for (int d = 0; d < N_DMA; ++d)
+          if (d * NMF / N_DMA == q) {
+            if (d < OX::kLoads) ox.load(rx, s, ax, d, wave);
+            else oy.load(ry, s + OX::kBytes, ay, d - OX::kLoads, wave);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  wait_loads();       // (loads past the end, which land as zeros)
+  __syncthreads();    // every wave's fragment reads are done
+
+  // The result passes through LDS, so that whole rows are stored: a block of
+  // the accumulators holds Z^T, 4 consecutive columns of one row per lane and
+  // register quad.  A tile that does not fit goes in EP passes of EJP blocks
+  // per wave.
+  constexpr int ESZ = static_cast<int>(sizeof(TOut));
+  constexpr int ERB = BN * ESZ, ECR = ERB / 16, EPC = 16 / ESZ;
+  constexpr int EP = (BM * ERB + 2 * STAGE - 1) / (2 * STAGE);
+  constexpr int EJP = FM / EP, EPR = BM / EP, ERI = 64 * kNW / ECR, EIT = EPR / ERI;
+  constexpr int ESW = ECR < 32 ? ECR - 1 : 31;
+  static_assert(FM % EP == 0 && EPR * ERB <= 2 * STAGE && 32 % ERI == 0, "staged store shape");
+  const int e_r = tid / ECR, e_c = tid % ECR;
+  const bool whole = i0 + BM <= I && j0 + BN <= a.J;
+#pragma unroll
+  for (int p = 0; p < EP; ++p) {
+    if (p > 0) __syncthreads();
+#pragma unroll
+    for (int jj = 0; jj < EJP; ++jj) {
+      const int j = p * EJP + jj;
+      const int lr = wm * 32 * EJP + jj * 32 + (lane & 31);
+      char* srow = smem + lr * ERB;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = {acc[i][j][4 * q + 0], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          const int byte = (wn * WTN + 32 * i + 8 * q + 4 * (lane >> 5)) * ESZ;
+          char* d = srow + (((byte >> 4) ^ (lr & ESW)) << 4) + (byte & 15);
+          if constexpr (ESZ == 4) {
+            *reinterpret_cast<f32x4*>(d) = v;
+          } else {
+            bf16x4 hv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hv[e] = static_cast<__bf16>(v[e]);
+            *reinterpret_cast<bf16x4*>(d) = hv;
+          }
+        }
+      }
     }
     __syncthreads();
 #pragma unroll
-    for (int l = 0; l < BL; l += 16) {
-      const bf16x8 fx = *reinterpret_cast<const bf16x8*>(shx + (wi + r) * ROW + l + 8 * h);
-      const bf16x8 fy = *reinterpret_cast<const bf16x8*>(shy + (wj + r) * ROW + l + 8 * h);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy, fx, acc, 0, 0, 0);
+    for (int it = 0; it < EIT; ++it) {
+      const int lr = ERI * it + e_r;
+      const u32x4 raw = *reinterpret_cast<const u32x4*>(smem + lr * ERB + ((e_c ^ (lr & ESW)) << 4));
+      const int i = i0 + ((ERI * it) / (32 * EJP)) * WTM + 32 * (p * EJP + ((ERI * it) / 32) % EJP) + (ERI * it) % 32 + e_r;
+      const int j = j0 + EPC * e_c;
+      TOut* dst = z + static_cast<int64_t>(i) * a.ldz + j;
+      if (whole || (i < I && j + EPC <= a.J)) {
+        __builtin_nontemporal_store(raw, reinterpret_cast<u32x4*>(dst));
+      } else if (i < I) {
+        const TOut* src = reinterpret_cast<const TOut*>(&raw);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e)
+          if (j + e < a.J) dst[e] = src[e];
+      }
     }
   }
-  const int64_t i = i0 + wi + r;
-  if (i >= I) return;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int j = j0 + wj + 8 * (q / 4) + 4 * h + q % 4;
-    if (j < a.J) z[i * a.zi + j] = static_cast<TOut>(acc[q]);
-  }
+}
+
+template <int BM, int BN, bool XC, bool YC>
+hipError_t launch_tiles(RArgs& r, bool f32, int64_t tiles_i, hipStream_t s) {
+  r.tiles_j = (r.J + BN - 1) / BN;
+  const int64_t tiles = tiles_i * r.tiles_j;
+  if (tiles > 0x7ffffff0) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(XC ? tiles : (tiles + 7) / 8 * 8));
+  if (f32) ragged_kernel<BM, BN, XC, YC, float><<<grid, 64 * kNW, 0, s>>>(r);
+  else ragged_kernel<BM, BN, XC, YC, __bf16><<<grid, 64 * kNW, 0, s>>>(r);
+  return hipGetLastError();
+}
+
+// 256 x 256 tiles where there are enough of them for the 256 compute units,
+// 128 x 128 tiles otherwise.  The count of row tiles is that of even experts:
+// the host does not know the offsets.
+template <bool XC, bool YC>
+hipError_t launch_form(RArgs& r, bool f32, hipStream_t s) {
+  auto tiles_i = [&](int64_t bm) {      // tile rows there can be
+    return XC ? r.experts * ((r.I + bm - 1) / bm) : r.T / bm + std::min<int64_t>(r.experts, r.T);
+  };
+  auto even = [&](int64_t bm) {
+    return XC ? tiles_i(bm) : r.experts * ((r.T / r.experts + bm - 1) / bm);
+  };
+  if (even(256) * ((r.J + 255) / 256) >= 256) return launch_tiles<256, 256, XC, YC>(r, f32, tiles_i(256), s);
+  return launch_tiles<128, 128, XC, YC>(r, f32, tiles_i(128), s);
 }
 
 }  // namespace
@@ -113,35 +505,35 @@ cce_status launch_ragged(const RaggedLaunch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   RArgs r{};
   r.offsets = L.offsets;
-  r.T = L.T;
+  r.T = static_cast<int>(L.T);
   r.experts = L.experts;
-  r.rows_i = L.kind != RAGGED_WGRAD;
   const __bf16* a = static_cast<const __bf16*>(L.a);
   const __bf16* b = static_cast<const __bf16*>(L.b);
   const __bf16* c = static_cast<const __bf16*>(L.c);
+  const int N = static_cast<int>(L.N), K = static_cast<int>(L.K);
+  const int lda = static_cast<int>(L.lda), ldb = static_cast<int>(L.ldb), ldc = static_cast<int>(L.ldc);
+  const bool f32 = L.out_t == CCE_F32;
+  hipError_t e;
   if (L.kind == RAGGED_FORWARD) {
-    r.x = a; r.xi = L.lda; r.xl = 1;
-    r.y = b; r.yj = L.ldb; r.yl = 1; r.ye = L.stride_b;
-    r.z = L.c; r.zi = L.ldc;
-    r.J = static_cast<int>(L.N); r.L = static_cast<int>(L.K);
+    r.x = a; r.ldx = lda;
+    r.y = b; r.ldy = ldb; r.ye = L.stride_b;
+    r.z = L.c; r.ldz = ldc;
+    r.J = N; r.L = K;
+    e = launch_form<false, false>(r, f32, s);
   } else if (L.kind == RAGGED_DGRAD) {
-    r.x = c; r.xi = L.ldc; r.xl = 1;
-    r.y = b; r.yj = 1; r.yl = L.ldb; r.ye = L.stride_b;
-    r.z = L.a; r.zi = L.lda;
-    r.J = static_cast<int>(L.K); r.L = static_cast<int>(L.N);
+    r.x = c; r.ldx = ldc;
+    r.y = b; r.ldy = ldb; r.ye = L.stride_b;
+    r.z = L.a; r.ldz = lda;
+    r.J = K; r.L = N;
+    e = launch_form<false, true>(r, f32, s);
   } else {
-    r.x = c; r.xi = 1; r.xl = L.ldc;
-    r.y = a; r.yj = 1; r.yl = L.lda;
-    r.z = L.b; r.zi = L.ldb; r.ze = L.stride_b;
-    r.I = static_cast<int>(L.N); r.J = static_cast<int>(L.K);
+    r.x = c; r.ldx = ldc;
+    r.y = a; r.ldy = lda;
+    r.z = L.b; r.ldz = ldb; r.ze = L.stride_b;
+    r.I = N; r.J = K;
+    e = launch_form<true, true>(r, f32, s);
   }
-  r.tiles_j = (r.J + 63) / 64;
-  const int64_t tiles_i = r.rows_i ? L.T / 64 + L.experts : static_cast<int64_t>(L.experts) * ((r.I + 63) / 64);
-  if (tiles_i * r.tiles_j > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "ragged GEMM: too many output tiles");
-  const dim3 grid(static_cast<unsigned>(tiles_i * r.tiles_j));
-  if (L.out_t == CCE_F32) ragged_kernel<float><<<grid, 256, 0, s>>>(r);
-  else ragged_kernel<__bf16><<<grid, 256, 0, s>>>(r);
-  const hipError_t e = hipGetLastError();
+  if (e == hipErrorInvalidValue) return fail(CCE_EUNSUPPORTED, "ragged GEMM: too many output tiles");
   if (e != hipSuccess) return fail(CCE_EHIP, std::string("ragged GEMM launch: ") + hipGetErrorString(e));
   return CCE_OK;
 }
