@@ -2,7 +2,15 @@
 //
 //   C[m, n] = sum_k (A[m, k] 2^(sa[m, k/128] - 127)) (B^T[n, k] 2^(sb[n/128, k/128] - 127))
 //
-// with fp32 accumulation and an optional GELU on the store.
+// with fp32 accumulation and an optional GELU on the store.  Three kernels:
+//
+//   gemm8_kernel       bf16 results, many rows: the matrix cores' 8-bit
+//                      instruction, which takes the scales as operands.
+//   gemm8_wide_kernel  fp32 results: e4m3 widened to bf16 on the way to the
+//                      matrix cores, because the 8-bit instruction's own sums
+//                      of 64 products keep about 16 bits (measured: 1.5e-5
+//                      of the result's norm against 1e-7).
+//   gemm8_rows_kernel  few rows: bound by reading B once; widened too.
 
 #include <hip/hip_runtime.h>
 
@@ -19,7 +27,15 @@ namespace cce {
 namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
+constexpr uint32_t kOob = 0x40000000;      // past every buffer below
+constexpr int kNontemporal = 2;            // buffer instruction cache policy
+constexpr int kBK = 128;                   // bytes of the contraction per tile: one scale block
 
 struct G8Args {
   const uint8_t* a;
@@ -27,10 +43,22 @@ struct G8Args {
   const uint8_t* sa;
   const uint8_t* sb;
   void* c;
-  int M, N, K, tiles_n;
-  int64_t lda, ldb, ldc, ld_sa, ld_sb;
+  int M, N, K, tiles_m, tiles_n;
+  int lda, ldb, ldc, ld_sa, ld_sb;
   bool gelu;
 };
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const int n = static_cast<int>(min(bytes, static_cast<int64_t>(kOob) - 256));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferFlags);
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t voffset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds, 16, voffset, 0, 0, 0);
+}
+// s_waitcnt vmcnt(0), the other counters left alone.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // 8 e4m3 values times their block's scale, as bf16.  The instruction takes
 // the scale as a float's exponent, which is E8M0's own encoding.  Exact: a
@@ -50,12 +78,207 @@ __device__ __forceinline__ bf16x8 scaled(u32x2 v, float scale) {
   return r;
 }
 
-__device__ __forceinline__ float scale_float(uint8_t s) {
-  return __builtin_bit_cast(float, static_cast<uint32_t>(s) << 23);
+__device__ __forceinline__ float scale_float(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+
+// Tile of a workgroup: each of the 8 XCDs (dealt workgroups in turn) gets a
+// contiguous range of tiles, walked in bands of 4 tile rows, so that the
+// tiles in flight share A and B rows in its L2.
+__device__ __forceinline__ void find_tile(const G8Args& a, int& tm, int& tn) {
+  const int w = blockIdx.x, per = gridDim.x / 8;
+  const int t = w < per * 8 ? (w & 7) * per + (w >> 3) : w;
+  constexpr int kBand = 4;
+  const int band = t / (kBand * a.tiles_n);
+  const int in_band = t - band * kBand * a.tiles_n;
+  const int height = min(a.tiles_m - band * kBand, kBand);
+  tm = band * kBand + in_band % height;
+  tn = in_band / height;
 }
 
+// ---------------------------------------------------------------------------
+// bf16 results on v_mfma_scale_f32_32x32x64_f8f6f4.
+//
+// The grouped GEMM's design (gemm.hip) at one byte per element: BM x BN x 128
+// tiles, LDS rows of 128 bytes in XOR-swizzled 16-byte chunks, two stages
+// filled by direct global-to-LDS loads, 4 waves of (BM/2) x (BN/2).  A tile
+// of the contraction is exactly one block of scales: the instruction takes
+// each lane's row scale as an operand, so the scales cost no arithmetic.  Per
+// tile two steps of 64:
+//   step 0: MFMA | fragment reads of step 1
+//   wait for the next tile's loads, barrier
+//   step 1: MFMA | fragment reads of the next tile | loads of the tile after
+//           next into this tile's buffer
+// ---------------------------------------------------------------------------
+template <int BM, int BN, bool GELU>
+__global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
+  constexpr int NW = 4, WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
+  constexpr int A_BYTES = BM * kBK, STAGE = (BM + BN) * kBK;
+  constexpr int A_DMA = BM / 32, B_DMA = BN / 32, N_DMA = A_DMA + B_DMA;   // 8 rows per instruction
+  static_assert(WTN <= 128 && 128 % WTN == 0, "one scale of B per wave");
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+
+  int tm, tn;
+  find_tile(a, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const __amdgpu_buffer_rsrc_t ra =
+      make_rsrc(a.a + static_cast<int64_t>(m0) * a.lda, static_cast<int64_t>(min(a.M - m0, BM) - 1) * a.lda + a.K);
+  const __amdgpu_buffer_rsrc_t rb =
+      make_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<int64_t>(min(a.N - n0, BN) - 1) * a.ldb + a.K);
+
+  // Loads: instruction p of wave w fills rows 8 (4 p + w) + lane / 8; rows
+  // past the end are out of the buffer's range, chunks past K steered there.
+  const int dl_row = 8 * wave + (lane >> 3);
+  const int dl_chunk = (lane & 7) ^ swz(dl_row);
+  const uint32_t off_a = static_cast<uint32_t>(dl_row) * a.lda + 16u * dl_chunk;
+  const uint32_t off_b = static_cast<uint32_t>(dl_row) * a.ldb + 16u * dl_chunk;
+  auto add_of = [&](int k0) { return k0 + (k0 + 16 * dl_chunk < a.K ? 0u : kOob); };
+  auto load = [&](int buf, uint32_t add, int d) {
+    char* s = smem + buf * STAGE + wave * 1024;
+    if (d < A_DMA) dma16(ra, s + d * NW * 1024, off_a + add + 32u * d * a.lda);
+    else dma16(rb, s + A_BYTES + (d - A_DMA) * NW * 1024, off_b + add + 32u * (d - A_DMA) * a.ldb);
+  };
+
+  // Fragments: row lane & 31 of a block, 32 bytes of the step's 64.
+  const int r = lane & 31, h = lane >> 5;
+  const int fa0 = (wm * WTM + r) * kBK, fb0 = A_BYTES + (wn * WTN + r) * kBK;
+  int fsw[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) fsw[q] = ((4 * (q >> 1) + 2 * h + (q & 1)) ^ swz(r)) << 4;
+  i32x8 fa[2][FM], fb[2][FN];
+  // half f & 1 of fragment f / 2 of step kk: B blocks first
+  auto fread = [&](int buf, int kk, int slot, int f) {
+    const int q = f >> 1, e = f & 1;
+    const char* s = smem + buf * STAGE + (q < FN ? fb0 + q * 32 * kBK : fa0 + (q - FN) * 32 * kBK);
+    const u32x4 v = *reinterpret_cast<const u32x4*>(s + fsw[2 * kk + e]);
+    i32x8& d = q < FN ? fb[slot][q] : fa[slot][q - FN];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[4 * e + i] = static_cast<int>(v[i]);
+  };
+
+  // Scales: byte of the lane's row per block of A, one byte per wave of B.
+  const uint8_t* sa[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+    sa[j] = a.sa + static_cast<int64_t>(min(m0 + wm * WTM + 32 * j + r, a.M - 1)) * a.ld_sa;
+  const uint8_t* sb = a.sb + static_cast<int64_t>(min(n0 + wn * WTN, a.N - 1) / 128) * a.ld_sb;
+  int va[FM], vb = 0;
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+  auto mfma = [&](int slot, int q) {
+    const int i = q / FM, j = (i & 1) ? FM - 1 - q % FM : q % FM;
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[slot][i], fa[slot][j], acc[i][j], 0, 0, 0, vb, 0, va[j]);
+  };
+
+  constexpr int NMF = FM * FN, NRD = 2 * (FM + FN);
+  const int KT = (a.K + kBK - 1) / kBK;
+  if (KT > 0) {
+#pragma unroll
+    for (int d = 0; d < N_DMA; ++d) load(0, add_of(0), d);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) va[j] = sa[j][0];
+    vb = sb[0];
+    wait_loads();
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < NRD; ++f) fread(0, 0, 0, f);
+#pragma unroll
+    for (int d = 0; d < N_DMA; ++d) load(1, add_of(kBK), d);
+  }
+  for (int kt = 0; kt < KT; ++kt) {
+    const int cur = kt & 1, nxt = cur ^ 1;
+    int na[FM], nb;
+    const int next = min(kt + 1, KT - 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < NMF; ++q) {
+      mfma(0, q);
+#pragma unroll
+      for (int f = 0; f < NRD; ++f)
+        if (f * NMF / NRD == q) fread(cur, 1, 1, f);
+      if (q == 0) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) na[j] = sa[j][next];
+        nb = sb[next];
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_loads();
+    __syncthreads();
+    const uint32_t add = add_of((kt + 2) * kBK);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < NMF; ++q) {
+      mfma(1, q);
+#pragma unroll
+      for (int f = 0; f < NRD; ++f)
+        if (f * NMF / NRD == q) fread(nxt, 0, 0, f);
+#pragma unroll
+      for (int d = 0; d < N_DMA; ++d)
+        if (d * NMF / N_DMA == q) load(cur, add, d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) va[j] = na[j];
+    vb = nb;
+  }
+  wait_loads();       // (loads past K, which land as zeros)
+  __syncthreads();    // every wave's fragment reads are done
+
+  // The result passes through LDS, so that whole rows are stored: a block of
+  // the accumulators holds C^T, 4 consecutive columns of one row per lane and
+  // register quad.
+  constexpr int ERB = BN * 2, ECR = ERB / 16, ERI = 64 * NW / ECR, EIT = BM / ERI;
+  constexpr int ESW = ECR < 32 ? ECR - 1 : 31;
+  static_assert(BM * ERB <= 2 * STAGE && 32 % ERI == 0, "staged store");
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int lr = wm * WTM + 32 * j + r;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = acc[i][j][4 * q + e];
+          if (GELU) x = gelu_exact(x);
+          v[e] = static_cast<__bf16>(x);
+        }
+        const int byte = (wn * WTN + 32 * i + 8 * q + 4 * h) * 2;
+        *reinterpret_cast<bf16x4*>(smem + lr * ERB + (((byte >> 4) ^ (lr & ESW)) << 4) + (byte & 15)) = v;
+        __builtin_amdgcn_sched_barrier(0);   // (one quad at a time: all at once spill)
+      }
+    }
+  }
+  __syncthreads();
+  const int e_r = tid / ECR, e_c = tid % ECR;
+  const int n = n0 + 8 * e_c;
+#pragma unroll
+  for (int it = 0; it < EIT; ++it) {
+    const int lr = ERI * it + e_r, m = m0 + lr;
+    const u32x4 raw = *reinterpret_cast<const u32x4*>(smem + lr * ERB + ((e_c ^ (lr & ESW)) << 4));
+    __bf16* dst = reinterpret_cast<__bf16*>(a.c) + static_cast<int64_t>(m) * a.ldc + n;
+    if (m < a.M && n + 8 <= a.N) {
+      __builtin_nontemporal_store(raw, reinterpret_cast<u32x4*>(dst));
+    } else if (m < a.M) {
+      const bf16x8 v = __builtin_bit_cast(bf16x8, raw);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < a.N) dst[e] = v[e];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // 64 x 64 tiles, one block of 128 of the contraction at a time: both operands
 // through LDS as they are, widened to bf16 on the way to the matrix cores.
+// ---------------------------------------------------------------------------
 template <typename TOut>
 __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
   constexpr int BM = 64, BN = 64, ROW = 128 + 16;
@@ -103,18 +326,162 @@ __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (M <= 16 FM): the time is that of reading B once.  A workgroup
+// takes 16 columns; its WAVES waves take every WAVES-th block of 128 of the
+// contraction, straight from memory to registers, two blocks ahead, and join
+// their sums through LDS in the order of the waves.  v_mfma_f32_16x16x32_bf16:
+// lane l holds row l & 15 and the 16-byte chunks l / 16 and l / 16 + 4 of a
+// block, so a load instruction reads 64 consecutive bytes of 16 rows; each
+// chunk feeds two instructions of 32 (which k go together is the same for
+// both operands, so their order does not matter).
+// ---------------------------------------------------------------------------
+template <int FM, int WAVES, typename TOut>
+__global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
+  __shared__ f32x4 part[WAVES > 1 ? WAVES - 1 : 1][FM][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int KB = (a.K + 127) / 128;
+  // Rows past the end and chunks past K are out of the buffers' range: zeros.
+  const __amdgpu_buffer_rsrc_t rb =
+      make_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<int64_t>(min(a.N - n0, 16) - 1) * a.ldb + a.K);
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.a, static_cast<int64_t>(a.M - 1) * a.lda + a.K);
+  const uint32_t off_b = n0 + r < a.N ? static_cast<uint32_t>(r) * a.ldb : kOob;
+  const uint8_t* sb = a.sb + static_cast<int64_t>(n0 / 128) * a.ld_sb;
+  uint32_t off_a[FM];
+  const uint8_t* sa[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int m = 16 * j + r;
+    off_a[j] = m < a.M ? static_cast<uint32_t>(m) * a.lda : kOob;
+    sa[j] = a.sa + static_cast<int64_t>(min(m, a.M - 1)) * a.ld_sa;
+  }
+  struct Block {
+    u32x4 b[2], a[FM][2];
+    uint32_t sb, sa[FM];
+  };
+  auto load = [&](Block& x, int kb) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int k = kb * 128 + 64 * c + 16 * g;
+      const uint32_t add = k + (k < a.K ? 0u : kOob);
+      x.b[c] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b + add, 0, kNontemporal);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) x.a[j][c] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[j] + add, 0, 0);
+    }
+    // (a block past the end is zeros times the last scale: a scale of NaN
+    // there has made the result NaN already)
+    const int s = min(kb, KB - 1);
+    x.sb = sb[s];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) x.sa[j] = sa[j][s];
+  };
+  f32x4 acc[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) acc[j] = f32x4{};
+  auto use = [&](const Block& x) {
+    const float fb = scale_float(x.sb);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bf16x8 vb = scaled(u32x2{x.b[c][2 * e], x.b[c][2 * e + 1]}, fb);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          const bf16x8 va = scaled(u32x2{x.a[j][c][2 * e], x.a[j][c][2 * e + 1]}, scale_float(x.sa[j]));
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, va, acc[j], 0, 0, 0);
+        }
+      }
+    }
+  };
+  if (wave < KB) {
+    constexpr int DEPTH = FM > 2 ? 2 : 4;      // blocks in flight per wave
+    Block x[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      load(x[d], wave + d * WAVES);
+      __builtin_amdgcn_sched_barrier(0);   // (in the loop's order, which its waits count on)
+    }
+    for (int kb = wave; kb < KB; kb += DEPTH * WAVES) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        use(x[d]);
+        load(x[d], kb + (d + DEPTH) * WAVES);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) part[wave - 1][j][lane] = acc[j];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    for (int w = 0; w < WAVES - 1; ++w) acc[j] = acc[j] + part[w][j][lane];
+    // the result block is C^T: the lane holds row r, columns 4 g + e
+    if (16 * j + r >= a.M) continue;
+    TOut* c = reinterpret_cast<TOut*>(a.c) + static_cast<int64_t>(16 * j + r) * a.ldc;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = n0 + 4 * g + e;
+      const float v = a.gelu ? gelu_exact(acc[j][e]) : acc[j][e];
+      if (n < a.N) c[n] = static_cast<TOut>(v);
+    }
+  }
+}
+
+template <int FM, int WAVES>
+void launch_rows(const G8Args& a, bool f32, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((a.N + 15) / 16));
+  if (f32) gemm8_rows_kernel<FM, WAVES, float><<<grid, 64 * WAVES, 0, s>>>(a);
+  else gemm8_rows_kernel<FM, WAVES, __bf16><<<grid, 64 * WAVES, 0, s>>>(a);
+}
+
+template <int FM>
+void launch_rows(const G8Args& a, bool f32, hipStream_t s) {
+  if (a.N > 4096) launch_rows<FM, 4>(a, f32, s);
+  else launch_rows<FM, 8>(a, f32, s);
+}
+
+template <int BM, int BN>
+void launch_tiles(G8Args a, hipStream_t s) {
+  a.tiles_m = (a.M + BM - 1) / BM;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  const dim3 grid(static_cast<unsigned>(a.tiles_m) * a.tiles_n);
+  if (a.gelu) gemm8_kernel<BM, BN, true><<<grid, 256, 0, s>>>(a);
+  else gemm8_kernel<BM, BN, false><<<grid, 256, 0, s>>>(a);
+}
+
 }  // namespace
 
 cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  G8Args a{L.a, L.b, L.sa, L.sb, L.c, static_cast<int>(L.M), static_cast<int>(L.N), static_cast<int>(L.K), 0,
-           L.lda, L.ldb, L.ldc, L.ld_sa, L.ld_sb, L.gelu};
-  a.tiles_n = static_cast<int>((L.N + 63) / 64);
-  const int64_t tiles = (L.M + 63) / 64 * a.tiles_n;
-  if (tiles > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
-  const dim3 grid(static_cast<unsigned>(tiles));
-  if (L.out_t == CCE_F32) gemm8_wide_kernel<float><<<grid, 256, 0, s>>>(a);
-  else gemm8_wide_kernel<__bf16><<<grid, 256, 0, s>>>(a);
+  G8Args a{L.a, L.b, L.sa, L.sb, L.c, static_cast<int>(L.M), static_cast<int>(L.N), static_cast<int>(L.K), 0, 0,
+           static_cast<int>(L.lda), static_cast<int>(L.ldb), static_cast<int>(L.ldc), static_cast<int>(L.ld_sa),
+           static_cast<int>(L.ld_sb), L.gelu};
+  auto tiles = [&](int64_t b) { return ((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
+  if (tiles(64) > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
+  const bool f32 = L.out_t == CCE_F32;
+  if (L.M <= 16) {
+    launch_rows<1>(a, f32, s);
+  } else if (L.M <= 32) {
+    launch_rows<2>(a, f32, s);
+  } else if (L.M <= 64) {
+    launch_rows<4>(a, f32, s);
+  } else if (!f32 && tiles(256) >= 256) {
+    launch_tiles<256, 256>(a, s);
+  } else if (!f32 && tiles(128) >= 64) {
+    launch_tiles<128, 128>(a, s);
+  } else {
+    a.tiles_n = static_cast<int>((L.N + 63) / 64);
+    const dim3 grid(static_cast<unsigned>((L.M + 63) / 64 * a.tiles_n));
+    if (f32) gemm8_wide_kernel<float><<<grid, 256, 0, s>>>(a);
+    else gemm8_wide_kernel<__bf16><<<grid, 256, 0, s>>>(a);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(CCE_EHIP, std::string("block-scaled GEMM launch: ") + hipGetErrorString(e));
   return CCE_OK;
