@@ -52,18 +52,21 @@ def _dtype(x) -> int:
     return int(x)
 
 
-def _mat(t: torch.Tensor) -> cce_mat:
+def _extent(t: torch.Tensor) -> tuple:
+    """(rows, cols, ld) of a 2-D tensor with unit column stride."""
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("tensor must have unit column stride")
-    if t.shape[1] == 0:
-        ld = 0                                   # empty rows: no element is addressed
-    elif t.shape[0] > 1:
-        ld = t.stride(0)
-    else:
-        ld = max(t.shape[1], t.stride(0))
-    return cce_mat(t.shape[0], t.shape[1], ld)
+    if cols == 0:
+        return rows, 0, 0                        # empty rows: no element is addressed
+    return rows, cols, ld if rows > 1 else max(cols, ld)
+
+
+def _mat(t: torch.Tensor) -> cce_mat:
+    return cce_mat(*_extent(t))
 
 
 def _same(ts, what):
@@ -90,13 +93,14 @@ def _on_device(ctx, ts):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda or (dev is not None and t.device.index != dev):
+        at = t.get_device()                      # -1: host memory
+        if at < 0 or (dev is not None and at != dev):
             raise ValueError(f"every tensor must be on cuda:{dev}, got one on {t.device}")
 
 
 def _stream(stream, device) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:                           # the current one's handle, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -471,7 +475,7 @@ _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
 def _shape_is(t, shape, what):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -482,10 +486,10 @@ def _vector(t, n, what):
 
 
 def _scales(t, rows, cols, block_rows, what):
-    """E8M0 scales of a [rows, cols] matrix in block_rows x 128 blocks."""
+    """ld of the E8M0 scales of a [rows, cols] matrix in block_rows x 128 blocks."""
     _dtype_is([t], _E8M0, what)
     _shape_is(t, (-(-rows // block_rows), -(-cols // 128)), what)
-    return _mat(t)
+    return _extent(t)[2]
 
 
 def _ptr(t):
@@ -497,24 +501,23 @@ def cce_rmsnorm(ctx: Context, x, weight, out, eps: float = 1e-5, residual=None, 
     """r = x + residual (rounded to x's dtype); out = r / sqrt(mean(r^2) + eps) * weight, row by
     row.  out: float32, bfloat16, or float8_e4m3fn with scales (float8_e8m0fnu, one per row and
     128 columns).  residual_out, if given, receives r."""
-    xm, om = _mat(x), _mat(out)
-    same = [t for t in (residual, residual_out) if t is not None]
-    _dtype_is(same, x.dtype, "the residual")
+    rows, cols, ld = _extent(x)
+    _dtype_is([residual, residual_out], x.dtype, "the residual")
     for t, what in ((residual, "residual"), (residual_out, "residual_out"), (out, "out")):
         if t is not None:
             _shape_is(t, x.shape, what)
-    _vector(weight, xm.cols, "weight")
+    _vector(weight, cols, "weight")
     quantized = out.dtype == _E4M3
     if quantized != (scales is not None):
         raise ValueError("scales go with a float8_e4m3fn output")
-    sm = _scales(scales, xm.rows, xm.cols, 1, "scales") if quantized else cce_mat(0, 0, 0)
-    rm = _mat(residual) if residual is not None else xm
-    rom = _mat(residual_out) if residual_out is not None else xm
+    ld_s = _scales(scales, rows, cols, 1, "scales") if quantized else 0
     _on_device(ctx, [x, weight, out, residual, residual_out, scales])
     check(lib().cce_rmsnorm(
-        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, _ptr(residual), rm.ld, _ptr(residual_out),
-        rom.ld, weight.data_ptr(), _dtype(weight.dtype), float(eps), out.data_ptr(),
-        CCE_E4M3 if quantized else _dtype(out.dtype), om.ld, _ptr(scales), sm.ld, 0,
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), _ptr(residual),
+        ld if residual is None else _extent(residual)[2], _ptr(residual_out),
+        ld if residual_out is None else _extent(residual_out)[2], weight.data_ptr(),
+        _dtype(weight.dtype), float(eps), out.data_ptr(),
+        CCE_E4M3 if quantized else _dtype(out.dtype), _extent(out)[2], _ptr(scales), ld_s, 0,
         _stream(stream, out.device)), "cce_rmsnorm")
     return out
 
@@ -531,23 +534,23 @@ def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: f
                          d_residual=None, workspace=None, stream=None):
     """Gradients of cce_rmsnorm for its normalised tensor x (residual_out where a residual was
     added): dx, of both summands, with d_residual added; dweight (float32), if given."""
-    xm = _mat(x)
+    rows, cols, ld = _extent(x)
     _dtype_is([dout, dx, d_residual], x.dtype, "dout, dx and d_residual")
     for t, what in ((dout, "dout"), (dx, "dx"), (d_residual, "d_residual")):
         if t is not None:
             _shape_is(t, x.shape, what)
-    _vector(weight, xm.cols, "weight")
+    _vector(weight, cols, "weight")
     if dweight is not None:
         _dtype_is([dweight], torch.float32, "dweight")
-        _vector(dweight, xm.cols, "dweight")
+        _vector(dweight, cols, "dweight")
     _on_device(ctx, [x, weight, dout, dx, dweight, d_residual, workspace])
-    rm = _mat(d_residual) if d_residual is not None else xm
     ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(x.shape), dx.device, workspace,
                          stream)
     check(lib().cce_rmsnorm_backward(
-        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, weight.data_ptr(), _dtype(weight.dtype),
-        dout.data_ptr(), _mat(dout).ld, _ptr(d_residual), rm.ld, float(eps), dx.data_ptr(),
-        _mat(dx).ld, _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), weight.data_ptr(),
+        _dtype(weight.dtype), dout.data_ptr(), _extent(dout)[2], _ptr(d_residual),
+        ld if d_residual is None else _extent(d_residual)[2], float(eps), dx.data_ptr(),
+        _extent(dx)[2], _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
         "cce_rmsnorm_backward")
     return dx
 
@@ -555,16 +558,16 @@ def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: f
 def cce_quantize_blocks(ctx: Context, x, q, scales, block_rows: int = 1, stream=None):
     """q (float8_e4m3fn) and scales (float8_e8m0fnu) of x in blocks of block_rows x 128:
     block_rows 1 for left operands, 128 for right operands of cce_block_scaled_gemm."""
-    xm, qm = _mat(x), _mat(q)
+    rows, cols, ld = _extent(x)
     _dtype_is([q], _E4M3, "q")
     _shape_is(q, x.shape, "q")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    sm = _scales(scales, xm.rows, xm.cols, block_rows, "scales")
+    ld_s = _scales(scales, rows, cols, block_rows, "scales")
     _on_device(ctx, [x, q, scales])
     check(lib().cce_quantize_blocks(
-        ctx.handle, _dtype(x.dtype), x.data_ptr(), xm, block_rows, q.data_ptr(), qm.ld,
-        scales.data_ptr(), sm.ld, 0, _stream(stream, q.device)), "cce_quantize_blocks")
+        ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), block_rows,
+        q.data_ptr(), _extent(q)[2], scales.data_ptr(), ld_s, 0, _stream(stream, q.device)), "cce_quantize_blocks")
     return q
 
 
@@ -574,12 +577,12 @@ def cce_block_scaled_gemm(ctx: Context, a, a_scales, b, b_scales, c, gelu: bool 
     b [N, K] with a scale per 128 x 128 block."""
     am, bm, cm = _mat(a), _mat(b), _mat(c)
     _dtype_is([a, b], _E4M3, "a and b")
-    sam = _scales(a_scales, am.rows, am.cols, 1, "a_scales")
-    sbm = _scales(b_scales, bm.rows, bm.cols, 128, "b_scales")
+    ld_sa = _scales(a_scales, am.rows, am.cols, 1, "a_scales")
+    ld_sb = _scales(b_scales, bm.rows, bm.cols, 128, "b_scales")
     _on_device(ctx, [a, a_scales, b, b_scales, c])
     check(lib().cce_block_scaled_gemm(
-        ctx.handle, _dtype(c.dtype), a.data_ptr(), am, a_scales.data_ptr(), sam.ld, b.data_ptr(),
-        bm, b_scales.data_ptr(), sbm.ld, c.data_ptr(), cm, CCE_FLAG_GELU if gelu else 0,
+        ctx.handle, _dtype(c.dtype), a.data_ptr(), am, a_scales.data_ptr(), ld_sa, b.data_ptr(),
+        bm, b_scales.data_ptr(), ld_sb, c.data_ptr(), cm, CCE_FLAG_GELU if gelu else 0,
         _stream(stream, c.device)), "cce_block_scaled_gemm")
     return c
 
@@ -588,7 +591,12 @@ def _experts(b, what):
     """[experts, N, K] as one expert's matrix and the elements from one to the next."""
     if b.dim() != 3 or b.shape[0] < 1:
         raise ValueError(f"{what} must be [experts, N, K]")
-    return _mat(b[0]), (b.stride(0) if b.shape[0] > 1 else 0)
+    experts, n, k = b.shape
+    stride, ld, step = b.stride()
+    if k > 1 and step != 1:
+        raise ValueError("tensor must have unit column stride")
+    ld = 0 if k == 0 else ld if n > 1 else max(k, ld)
+    return cce_mat(n, k, ld), (stride if experts > 1 else 0)
 
 
 def _offsets(offsets, experts):

@@ -64,8 +64,10 @@ class _Fake:
 
     def __init__(self, shape, dtype):
         self._t = torch.empty(shape, dtype=dtype)
-        self.is_cuda = True
         self.device = torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
 
     def __getattr__(self, name):
         return getattr(self._t, name)
