@@ -14,6 +14,8 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <string>
+#include <type_traits>
 
 #include "cce_internal.hpp"
 #include "elem8.hpp"
@@ -36,17 +38,28 @@ struct NArgs {
   bool w_f32;
 };
 
-// Sum over the workgroup, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
+// Sum over the WAVES waves of a row, the same in every thread.  The threads'
+// sums, of 8 to 64 terms in fp32, are joined in fp64: the join's roundings
+// would be common to the whole row, and each flips the rounding of a few
+// e4m3 results.
+template <int WAVES>
+__device__ __forceinline__ double row_sum(float v, double* sh) {
+  double s = v;
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-  const int waves = blockDim.x >> 6;
-  __syncthreads();   // the previous sum's reads are done
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = sh[0];
-  for (int i = 1; i < waves; ++i) s += sh[i];
+  for (int m = 32; m >= 1; m >>= 1) s += __shfl_xor(s, m);
+  if constexpr (WAVES > 1) {
+    __syncthreads();   // the previous sum's reads are done
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = sh[0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) s += sh[i];
+  }
   return s;
+}
+
+__device__ __forceinline__ float rstd_of(double squares, int cols, float eps) {
+  return static_cast<float>(1.0 / sqrt(squares / cols + eps));
 }
 
 __device__ __forceinline__ void load_weight(const NArgs& a, int j, float (&w)[8]) {
@@ -59,11 +72,68 @@ __device__ __forceinline__ float rounded(float v) {
   return static_cast<float>(static_cast<T>(v));
 }
 
-// Maximum over a group of 16 lanes (128 columns).
+// Maximum over a group of 16 lanes (128 columns): rotations within the 16.
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(v, m)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x128, 0xf, 0xf, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x124, 0xf, 0xf, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x122, 0xf, 0xf, true)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x121, 0xf, 0xf, true)));
   return v;
+}
+
+// 8 columns as they are in memory: 1 (bf16) or 2 (fp32) vectors of 16 bytes.
+template <typename T>
+struct Raw {
+  u32x4 v[sizeof(T) / 2];
+};
+
+constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
+constexpr int kNontemporal = 2;            // buffer instruction cache policy
+
+// A row of n columns.  Its range ends with the 16-byte vector that holds
+// column n - 1 (ld is a multiple of 8, so that lies within the row's ld).
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* base, int64_t row, int64_t ld, int n) {
+  const T* p = reinterpret_cast<const T*>(base) + row * ld;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), (short)0,
+                                           static_cast<int>((n * static_cast<int>(sizeof(T)) + 15) & ~15), kBufferFlags);
+}
+
+// Vector i of a row; zeros past its range.
+template <typename T, bool NT>
+__device__ __forceinline__ Raw<T> load_raw(__amdgpu_buffer_rsrc_t r, int i) {
+  Raw<T> x;
+#pragma unroll
+  for (unsigned h = 0; h < sizeof(T) / 2; ++h)
+    x.v[h] = __builtin_amdgcn_raw_buffer_load_b128(r, i * 8 * static_cast<int>(sizeof(T)) + 16 * h, 0, NT ? kNontemporal : 0);
+  return x;
+}
+
+// Keeps a vector as it is in memory across a use: without it the compiler
+// holds the widened values instead, which take twice the registers (or more)
+// and spill.
+template <typename T>
+__device__ __forceinline__ void keep_raw(Raw<T>& x) {
+#pragma unroll
+  for (unsigned h = 0; h < sizeof(T) / 2; ++h) asm volatile("" : "+v"(x.v[h]));
+}
+
+// In float; columns from n on (of a row whose width is no multiple of 8) are
+// zero, whatever lies there.
+template <typename T>
+__device__ __forceinline__ void widen(const Raw<T>& x, int j, int n, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_bit_cast(f32x4, x.v[e / 4])[e % 4];
+  } else {
+    const bf16x8 b = __builtin_bit_cast(bf16x8, x.v[0]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(b[e]);
+  }
+  if (n & 7) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = j + e < n ? v[e] : 0.0f;
+  }
 }
 
 template <typename TX>
@@ -77,53 +147,103 @@ __device__ __forceinline__ void load_sum(const NArgs& a, int64_t row, int j, flo
   }
 }
 
-// One workgroup per row, two passes over it.
-template <typename TX, typename TO>
+// What follows the norm of vector i (all 16 lanes of its block of 128
+// columns): the product with the weight and the store, in TO or in e4m3.
+template <typename TO>
+__device__ __forceinline__ void finish(const NArgs& a, int64_t row, int i, const float (&v)[8], const float (&w)[8],
+                                       float rstd) {
+  const int j = 8 * i;
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = v[e] * rstd * w[e];
+  if constexpr (sizeof(TO) == 1) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, j + e < a.cols ? magnitude(y[e]) : 0u);
+    const uint32_t s = scale_of(max16(top));
+    const float inv = inverse_of(s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= inv;
+    if (j < a.cols) {
+      store8_e4m3(reinterpret_cast<uint8_t*>(a.out) + row * a.ld_out, j, a.cols, y);
+      if (i % 16 == 0) a.scales[row * a.ld_scales + i / 16] = static_cast<uint8_t>(s);
+    }
+  } else {
+    if (j < a.cols) store8(reinterpret_cast<TO*>(a.out) + row * a.ld_out, j, a.cols, y);
+  }
+}
+
+// The row in registers: one pass over the data, bound by HBM.  A row has
+// 256 / RPW threads with NV vectors each; all its loads (and the weight's)
+// are in flight before the first is used.
+template <typename TX, typename TW, typename TO, int RPW, int NV>
 __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NArgs a) {
-  __shared__ float sh[kThreads / 64];
+  constexpr int TPR = kThreads / RPW;
+  __shared__ double sh[kThreads / 64];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  if (row >= a.rows) return;      // (rows of a workgroup only share it where each is one wave)
+  const int t = threadIdx.x % TPR;
+  const __amdgpu_buffer_rsrc_t rx = row_rsrc<TX>(a.x, row, a.ld_x, a.cols);
+  const __amdgpu_buffer_rsrc_t rw = row_rsrc<TW>(a.w, 0, 0, a.cols);
+  Raw<TX> x[NV], r[NV];
+  Raw<TW> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = load_raw<TX, true>(rx, t + i * TPR);
+  if (a.res) {
+    const __amdgpu_buffer_rsrc_t rr = row_rsrc<TX>(a.res, row, a.ld_res, a.cols);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) r[i] = load_raw<TX, true>(rr, t + i * TPR);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i] = load_raw<TW, false>(rw, t + i * TPR);
+  float v[NV][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = 8 * (t + i * TPR);
+    widen(x[i], j, a.cols, v[i]);
+    if (a.res) {
+      float u[8];
+      widen(r[i], j, a.cols, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = rounded<TX>(v[i][e] + u[e]);
+      if (a.res_out && j < a.cols)
+        store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, j, a.cols, v[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += v[i][e] * v[i][e];
+  }
+  const float rstd = rstd_of(row_sum<TPR / 64>(ss, sh), a.cols, a.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float u[8];
+    widen(w[i], 8 * (t + i * TPR), a.cols, u);
+    finish<TO>(a, row, t + i * TPR, v[i], u, rstd);
+  }
+}
+
+// Rows too wide for the registers: one workgroup per row, two passes over it
+// (the second mostly from the caches).
+template <typename TX, typename TO>
+__global__ __launch_bounds__(kThreads) void rmsnorm_wide_kernel(NArgs a) {
+  __shared__ double sh[kThreads / 64];
   const int tid = threadIdx.x;
   const int vectors = (a.cols + 7) >> 3;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float ss = 0.0f;
-    for (int i = tid; i < vectors; i += kThreads) {
-      float v[8];
-      load_sum<TX>(a, row, 8 * i, v);
+  const int64_t row = blockIdx.x;
+  float ss = 0.0f;
+  for (int i = tid; i < vectors; i += kThreads) {
+    float v[8];
+    load_sum<TX>(a, row, 8 * i, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-      if (a.res_out)
-        store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, 8 * i, a.cols, v);
-    }
-    ss = block_sum(ss, sh);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    for (int i0 = 0; i0 < vectors; i0 += kThreads) {   // (every lane: the scale's maximum needs them)
-      const int i = i0 + tid;
-      float v[8], w[8];
-      if (i < vectors) {
-        load_sum<TX>(a, row, 8 * i, v);
-        load_weight(a, 8 * i, w);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.0f;
-      }
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = v[e] * rstd * w[e];
-      if constexpr (sizeof(TO) == 1) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, 8 * i + e < a.cols ? magnitude(y[e]) : 0u);
-        const uint32_t s = scale_of(max16(top));
-        const float inv = inverse_of(s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv;
-        if (i < vectors) {
-          store8_e4m3(reinterpret_cast<uint8_t*>(a.out) + row * a.ld_out, 8 * i, a.cols, y);
-          if (i % 16 == 0) a.scales[row * a.ld_scales + i / 16] = static_cast<uint8_t>(s);
-        }
-      } else {
-        if (i < vectors) store8(reinterpret_cast<TO*>(a.out) + row * a.ld_out, 8 * i, a.cols, y);
-      }
-    }
+    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+    if (a.res_out) store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, 8 * i, a.cols, v);
+  }
+  const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
+  for (int i0 = 0; i0 < vectors; i0 += kThreads) {   // (every lane: a scale's maximum needs its 16)
+    float v[8], w[8];
+    load_sum<TX>(a, row, 8 * (i0 + tid), v);
+    load_weight(a, 8 * (i0 + tid), w);
+    finish<TO>(a, row, i0 + tid, v, w, rstd);
   }
 }
 
@@ -143,50 +263,134 @@ struct BArgs {
   bool w_f32;
 };
 
+// One pass over the data: x and dout of a row stay in registers between its
+// two sums and its dx, and a thread keeps the sums of its columns of dw over
+// the rows its workgroup takes (every gridDim.x-th group of RPW); they go to
+// the workspace at the end, a line per group of threads, and column_sum_kernel
+// adds the lines in their order.
+template <typename TX, typename TW, int THREADS, int RPW, int NV>
+__global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
+  constexpr int TPR = THREADS / RPW;
+  __shared__ double sh[THREADS / 64], sh2[THREADS / 64];
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const int t = threadIdx.x % TPR;
+  const __amdgpu_buffer_rsrc_t rw = row_rsrc<TW>(a.w, 0, 0, a.cols);
+  Raw<TW> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i] = load_raw<TW, false>(rw, t + i * TPR);
+  float dw[NV][8] = {};
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + sub; row < a.rows;
+       row += static_cast<int64_t>(gridDim.x) * RPW) {
+    const __amdgpu_buffer_rsrc_t rx = row_rsrc<TX>(a.x, row, a.ld_x, a.cols);
+    const __amdgpu_buffer_rsrc_t rd = row_rsrc<TX>(a.dout, row, a.ld_dout, a.cols);
+    Raw<TX> x[NV], d[NV], r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = load_raw<TX, true>(rx, t + i * TPR);
+      d[i] = load_raw<TX, true>(rd, t + i * TPR);
+    }
+    if (a.dres) {
+      const __amdgpu_buffer_rsrc_t rr = row_rsrc<TX>(a.dres, row, a.ld_dres, a.cols);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) r[i] = load_raw<TX, true>(rr, t + i * TPR);
+    }
+    float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = 8 * (t + i * TPR);
+      float v[8], g[8], u[8];
+      widen(x[i], j, a.cols, v);
+      widen(d[i], j, a.cols, g);
+      widen(w[i], j, a.cols, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss += v[e] * v[e];
+        dot += g[e] * u[e] * v[e];
+      }
+      keep_raw(x[i]);
+      keep_raw(d[i]);
+      keep_raw(w[i]);
+      __builtin_amdgcn_sched_barrier(0);   // (one vector widened at a time)
+    }
+    const float rstd = rstd_of(row_sum<TPR / 64>(ss, sh), a.cols, a.eps);
+    const float mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2) / a.cols) * rstd;   // of w dy n
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = 8 * (t + i * TPR);
+      float v[8], g[8], u[8];
+      widen(x[i], j, a.cols, v);
+      widen(d[i], j, a.cols, g);
+      widen(w[i], j, a.cols, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float n = v[e] * rstd;
+        dw[i][e] += g[e] * n;
+        u[e] = (g[e] * u[e] - n * mean) * rstd;
+      }
+      if (a.dres) {
+        widen(r[i], j, a.cols, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] += g[e];
+      }
+      if (j < a.cols) store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, j, a.cols, u);
+      keep_raw(w[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (!a.dw) return;
+  float* p = a.part + (static_cast<int64_t>(blockIdx.x) * RPW + sub) * a.ld_part;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = 8 * (t + i * TPR);
+    if (j >= a.cols) continue;      // (ld_part is a multiple of 8)
+    *reinterpret_cast<f32x4*>(p + j) = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+    *reinterpret_cast<f32x4*>(p + j + 4) = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// Rows too wide for the registers: dx by two passes over each row, which also
+// leave 1 / root in the workspace, and dw by a pass of its own (below).
 template <typename TX>
-__global__ __launch_bounds__(kThreads) void rmsnorm_backward_rows_kernel(BArgs a) {
-  __shared__ float sh[kThreads / 64];
+__global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a) {
+  __shared__ double sh[kThreads / 64], sh2[kThreads / 64];
   const int tid = threadIdx.x;
   const int vectors = (a.cols + 7) >> 3;
   NArgs wa{};
   wa.w = a.w;
   wa.cols = a.cols;
   wa.w_f32 = a.w_f32;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const TX* x = reinterpret_cast<const TX*>(a.x) + row * a.ld_x;
-    const TX* dy = reinterpret_cast<const TX*>(a.dout) + row * a.ld_dout;
-    float ss = 0.0f, dot = 0.0f;
-    for (int i = tid; i < vectors; i += kThreads) {
-      float v[8], d[8], w[8];
-      load8(x, 8 * i, a.cols, v);
-      load8(dy, 8 * i, a.cols, d);
-      load_weight(wa, 8 * i, w);
+  const int64_t row = blockIdx.x;
+  const TX* x = reinterpret_cast<const TX*>(a.x) + row * a.ld_x;
+  const TX* dy = reinterpret_cast<const TX*>(a.dout) + row * a.ld_dout;
+  float ss = 0.0f, dot = 0.0f;
+  for (int i = tid; i < vectors; i += kThreads) {
+    float v[8], d[8], w[8];
+    load8(x, 8 * i, a.cols, v);
+    load8(dy, 8 * i, a.cols, d);
+    load_weight(wa, 8 * i, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss += v[e] * v[e];
-        dot += d[e] * w[e] * v[e];
-      }
+    for (int e = 0; e < 8; ++e) {
+      ss += v[e] * v[e];
+      dot += d[e] * w[e] * v[e];
     }
-    ss = block_sum(ss, sh);
-    dot = block_sum(dot, sh);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    const float mean = dot * rstd / static_cast<float>(a.cols);   // mean of w dy n
-    if (tid == 0) a.rstd[row] = rstd;
-    for (int i = tid; i < vectors; i += kThreads) {
-      float v[8], d[8], w[8], g[8];
-      load8(x, 8 * i, a.cols, v);
-      load8(dy, 8 * i, a.cols, d);
-      load_weight(wa, 8 * i, w);
+  }
+  const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
+  const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) / a.cols) * rstd;
+  if (tid == 0) a.rstd[row] = rstd;
+  for (int i = tid; i < vectors; i += kThreads) {
+    float v[8], d[8], w[8], g[8];
+    load8(x, 8 * i, a.cols, v);
+    load8(dy, 8 * i, a.cols, d);
+    load_weight(wa, 8 * i, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = (d[e] * w[e] - v[e] * rstd * mean) * rstd;
-      if (a.dres) {
-        float r[8];
-        load8(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, 8 * i, a.cols, r);
+    for (int e = 0; e < 8; ++e) g[e] = (d[e] * w[e] - v[e] * rstd * mean) * rstd;
+    if (a.dres) {
+      float r[8];
+      load8(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, 8 * i, a.cols, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] += r[e];
-      }
-      store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, 8 * i, a.cols, g);
+      for (int e = 0; e < 8; ++e) g[e] += r[e];
     }
+    store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, 8 * i, a.cols, g);
   }
 }
 
@@ -222,13 +426,22 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_dweight_kernel(BArgs a) {
   }
 }
 
-// dw = the sum of the partial sums, in the order of the chunks.
+// dw = the sum of the partial sums: 16 columns per workgroup of 16 x 16
+// threads, each thread every 16th line, then the 16 of a column in order.
 __global__ __launch_bounds__(kThreads) void column_sum_kernel(const float* part, int chunks, int ld_part,
                                                               float* dw, int cols) {
-  const int j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= cols) return;
+  __shared__ float sh[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int j = blockIdx.x * 16 + c;
   float s = 0.0f;
-  for (int c = 0; c < chunks; ++c) s += part[static_cast<int64_t>(c) * ld_part + j];
+  if (j < cols) {
+#pragma unroll 8
+    for (int i = r; i < chunks; i += 16) s += part[static_cast<int64_t>(i) * ld_part + j];
+  }
+  sh[r][c] = s;
+  __syncthreads();
+  if (r != 0 || j >= cols) return;
+  for (int i = 1; i < 16; ++i) s += sh[i][c];
   dw[j] = s;
 }
 
@@ -310,11 +523,65 @@ cce_status launched(const char* what) {
 
 constexpr int64_t kMaxRowGrid = 1 << 20;
 
-// Chunks of rows whose sums of dw are kept apart: enough workgroups for the
-// GPU, and few enough that the partial sums stay a small part of the traffic.
-int dweight_chunks(int64_t rows, int64_t cols) {
-  const int64_t wide = (cols + 511) / 512;
-  return static_cast<int>(std::max<int64_t>(1, std::min({rows / 16, int64_t{2048} / wide, int64_t{256}})));
+// Widest row that the kernels keep in registers (two tensors of it in the
+// backward pass; a fourth vector per thread spills there).
+constexpr int64_t kMaxForwardCols = 16384, kMaxBackwardCols = 12288;
+
+// Lines of partial sums of dw.  In registers: a line per row of a workgroup,
+// two workgroups per compute unit.  Wide: chunks of rows, enough for the GPU
+// and few enough that the lines stay a small part of the traffic.
+constexpr int64_t kBackwardGroups = 512;
+int backward_rows_per_group(int64_t cols) { return cols <= 1024 ? 4 : 1; }
+int dweight_lines(int64_t rows, int64_t cols) {
+  if (cols <= kMaxBackwardCols) {
+    const int rpw = backward_rows_per_group(cols);
+    return static_cast<int>(std::min(kBackwardGroups, (rows + rpw - 1) / rpw) * rpw);
+  }
+  return static_cast<int>(std::max<int64_t>(1, std::min({rows / 16, int64_t{64}})));
+}
+
+template <typename TX, typename TW, typename TO>
+void launch_norm(const NArgs& a, hipStream_t s) {
+  auto go = [&](auto rpw, auto nv) {
+    constexpr int RPW = decltype(rpw)::value, NV = decltype(nv)::value;
+    rmsnorm_kernel<TX, TW, TO, RPW, NV><<<dim3((a.rows + RPW - 1) / RPW), kThreads, 0, s>>>(a);
+  };
+  // A wave per row up to 1024 columns, a workgroup of four per row above.
+  if (a.cols <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  else if (a.cols <= 1024) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  else if (a.cols <= 2048) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  else if (a.cols <= 4096) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
+  else if (a.cols <= 8192) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
+  else if (a.cols <= 12288) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 6>{});
+  else if (a.cols <= kMaxForwardCols) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+  else rmsnorm_wide_kernel<TX, TO><<<dim3(a.rows), kThreads, 0, s>>>(a);
+}
+
+template <typename TX, typename TO>
+void launch_norm_w(const NArgs& a, hipStream_t s) {
+  if (a.w_f32) launch_norm<TX, float, TO>(a, s);
+  else launch_norm<TX, __bf16, TO>(a, s);
+}
+
+template <typename TX, typename TW>
+void launch_backward(const BArgs& a, hipStream_t s) {
+  auto go = [&](auto threads, auto rpw, auto nv) {
+    constexpr int T = decltype(threads)::value, RPW = decltype(rpw)::value, NV = decltype(nv)::value;
+    const int64_t groups = std::min<int64_t>(kBackwardGroups, (a.rows + RPW - 1) / RPW);
+    rmsnorm_backward_kernel<TX, TW, T, RPW, NV><<<dim3(static_cast<unsigned>(groups)), T, 0, s>>>(a);
+  };
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  using I4 = std::integral_constant<int, 4>;
+  using T256 = std::integral_constant<int, 256>;
+  using T512 = std::integral_constant<int, 512>;
+  if (a.cols <= 512) go(T256{}, I4{}, I1{});
+  else if (a.cols <= 1024) go(T256{}, I4{}, I2{});
+  else if (a.cols <= 2048) go(T256{}, I1{}, I1{});
+  else if (a.cols <= 4096) go(T512{}, I1{}, I1{});
+  else if (a.cols <= 8192) go(T512{}, I1{}, I2{});
+  else go(T512{}, I1{}, I3{});
 }
 
 }  // namespace
@@ -323,23 +590,27 @@ cce_status launch_rmsnorm(const NormLaunch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   NArgs a{L.x, L.res, L.res_out, L.w, L.out, L.scales, static_cast<int>(L.rows), static_cast<int>(L.cols),
           L.ld_x, L.ld_res, L.ld_res_out, L.ld_out, L.ld_scales, L.eps, L.w_t == CCE_F32};
-  const dim3 grid(static_cast<unsigned>(std::min(L.rows, kMaxRowGrid)));
   if (L.x_t == CCE_F32) {
-    if (L.out_t == CCE_E4M3) rmsnorm_kernel<float, e4m3><<<grid, kThreads, 0, s>>>(a);
-    else if (L.out_t == CCE_F32) rmsnorm_kernel<float, float><<<grid, kThreads, 0, s>>>(a);
-    else rmsnorm_kernel<float, __bf16><<<grid, kThreads, 0, s>>>(a);
+    if (L.out_t == CCE_E4M3) launch_norm_w<float, e4m3>(a, s);
+    else if (L.out_t == CCE_F32) launch_norm_w<float, float>(a, s);
+    else launch_norm_w<float, __bf16>(a, s);
   } else {
-    if (L.out_t == CCE_E4M3) rmsnorm_kernel<__bf16, e4m3><<<grid, kThreads, 0, s>>>(a);
-    else if (L.out_t == CCE_F32) rmsnorm_kernel<__bf16, float><<<grid, kThreads, 0, s>>>(a);
-    else rmsnorm_kernel<__bf16, __bf16><<<grid, kThreads, 0, s>>>(a);
+    if (L.out_t == CCE_E4M3) launch_norm_w<__bf16, e4m3>(a, s);
+    else if (L.out_t == CCE_F32) launch_norm_w<__bf16, float>(a, s);
+    else launch_norm_w<__bf16, __bf16>(a, s);
   }
   return launched("rmsnorm");
+}
+
+// Workspace: [rows] floats (wide rows), then the lines of partial sums.
+static int64_t rstd_bytes(int64_t rows, int64_t cols) {
+  return cols <= kMaxBackwardCols ? 0 : (rows * 4 + 255) & ~int64_t{255};
 }
 
 size_t rmsnorm_backward_bytes(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
   const int64_t ld = (cols + 7) & ~int64_t{7};
-  return static_cast<size_t>(((rows * 4 + 255) & ~int64_t{255}) + dweight_chunks(rows, cols) * ld * 4);
+  return static_cast<size_t>(rstd_bytes(rows, cols) + dweight_lines(rows, cols) * ld * 4);
 }
 
 cce_status launch_rmsnorm_backward(const NormBackwardLaunch& L, void* stream) {
@@ -348,29 +619,36 @@ cce_status launch_rmsnorm_backward(const NormBackwardLaunch& L, void* stream) {
   a.x = L.x; a.w = L.w; a.dout = L.dout; a.dres = L.dres; a.dx = L.dx; a.dw = L.dw;
   a.rows = static_cast<int>(L.rows);
   a.cols = static_cast<int>(L.cols);
-  a.chunks = dweight_chunks(L.rows, L.cols);
+  a.chunks = L.rows > 0 ? dweight_lines(L.rows, L.cols) : 0;
   a.ld_part = static_cast<int>((L.cols + 7) & ~int64_t{7});
   a.rstd = reinterpret_cast<float*>(L.workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(L.workspace) + ((L.rows * 4 + 255) & ~int64_t{255}));
+  a.part = reinterpret_cast<float*>(static_cast<char*>(L.workspace) + rstd_bytes(L.rows, L.cols));
   a.ld_x = L.ld_x; a.ld_dout = L.ld_dout; a.ld_dres = L.ld_dres; a.ld_dx = L.ld_dx;
   a.eps = L.eps;
   a.w_f32 = L.w_t == CCE_F32;
-  const unsigned cols_grid = static_cast<unsigned>((L.cols + kThreads - 1) / kThreads);
+  const bool xf = L.x_t == CCE_F32, wide = L.cols > kMaxBackwardCols;
   if (L.rows > 0) {
-    const dim3 grid(static_cast<unsigned>(std::min(L.rows, kMaxRowGrid)));
-    if (L.x_t == CCE_F32) rmsnorm_backward_rows_kernel<float><<<grid, kThreads, 0, s>>>(a);
-    else rmsnorm_backward_rows_kernel<__bf16><<<grid, kThreads, 0, s>>>(a);
+    if (wide) {
+      if (xf) rmsnorm_backward_wide_kernel<float><<<dim3(a.rows), kThreads, 0, s>>>(a);
+      else rmsnorm_backward_wide_kernel<__bf16><<<dim3(a.rows), kThreads, 0, s>>>(a);
+    } else if (xf) {
+      if (a.w_f32) launch_backward<float, float>(a, s);
+      else launch_backward<float, __bf16>(a, s);
+    } else {
+      if (a.w_f32) launch_backward<__bf16, float>(a, s);
+      else launch_backward<__bf16, __bf16>(a, s);
+    }
     if (const cce_status st = launched("rmsnorm backward"); st != CCE_OK) return st;
-    if (!L.dw) return CCE_OK;
-    const dim3 wgrid(static_cast<unsigned>((L.cols + 511) / 512), static_cast<unsigned>(a.chunks));
-    if (L.x_t == CCE_F32) rmsnorm_dweight_kernel<float><<<wgrid, kThreads, 0, s>>>(a);
-    else rmsnorm_dweight_kernel<__bf16><<<wgrid, kThreads, 0, s>>>(a);
-    if (const cce_status st = launched("rmsnorm weight gradient"); st != CCE_OK) return st;
-  } else {
-    a.chunks = 0;
+    if (wide && L.dw) {
+      const dim3 grid(static_cast<unsigned>((L.cols + 511) / 512), static_cast<unsigned>(a.chunks));
+      if (xf) rmsnorm_dweight_kernel<float><<<grid, kThreads, 0, s>>>(a);
+      else rmsnorm_dweight_kernel<__bf16><<<grid, kThreads, 0, s>>>(a);
+      if (const cce_status st = launched("rmsnorm weight gradient"); st != CCE_OK) return st;
+    }
   }
   if (!L.dw) return CCE_OK;
-  column_sum_kernel<<<dim3(cols_grid), kThreads, 0, s>>>(a.part, a.chunks, a.ld_part, a.dw, a.cols);
+  column_sum_kernel<<<dim3(static_cast<unsigned>((L.cols + 15) / 16)), kThreads, 0, s>>>(a.part, a.chunks, a.ld_part,
+                                                                                       a.dw, a.cols);
   return launched("rmsnorm weight gradient sum");
 }
 
