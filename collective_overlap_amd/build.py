@@ -71,11 +71,14 @@ COMMON = [
 # per lane this compiler gives them today: the 256 x 256 bf16 store without
 # GELU (the local partial GEMM) and the 256 x 256 bf16 accumulate without GELU
 # (only the last iteration of an AllGather case 2 with a bf16 output runs it),
-# two registers each.  Any other spill, or a larger one, fails the build: in a
+# two registers each; and the 256 x 256 8-bit product without GELU, one register
+# (the thread number, stored before the k loop and read back behind it).  Any
+# other spill, or a larger one, fails the build: in a
 # GEMM it would otherwise show only as an unexplained slowdown.
 KNOWN_SPILLS = {
     "_ZN3cce12_GLOBAL__N_116gemm_bf16_kernelILi256ELi256ELi2ELi2ELi64ELi2EDF16bLi0ELb0EEEvNS0_5KArgsE": 8,
     "_ZN3cce12_GLOBAL__N_116gemm_bf16_kernelILi256ELi256ELi2ELi2ELi64ELi2EDF16bLi1ELb0EEEvNS0_5KArgsE": 8,
+    "_ZN3cce12_GLOBAL__N_112gemm8_kernelILi256ELi256ELb0EEEvNS0_6G8ArgsE": 8,
 }
 
 

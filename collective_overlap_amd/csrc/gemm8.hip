@@ -30,7 +30,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef const __attribute__((address_space(3))) uint8_t* lds_bytes;
 
 constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x40000000;      // past every buffer below
@@ -46,6 +48,7 @@ struct G8Args {
   int M, N, K, tiles_m, tiles_n;
   int lda, ldb, ldc, ld_sa, ld_sb;
   bool gelu;
+  bool scale_words;     // both scale matrices' rows start on 4-byte words
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
@@ -59,6 +62,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char* lds, uint3
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// A byte of LDS.  (The restrict pointer gives the read alias information, which
+// a byte's type does not; without any the compiler takes it to depend on every
+// load to LDS in flight and waits for them.)
+__device__ __forceinline__ int read_byte(const __attribute__((address_space(3))) uint8_t* __restrict__ p) { return *p; }
 
 // 8 e4m3 values times their block's scale, as bf16.  The instruction takes
 // the scale as a float's exponent, which is E8M0's own encoding.  Exact: a
@@ -101,20 +109,27 @@ __device__ __forceinline__ void find_tile(const G8Args& a, int& tm, int& tn) {
 // tiles, LDS rows of 128 bytes in XOR-swizzled 16-byte chunks, two stages
 // filled by direct global-to-LDS loads, 4 waves of (BM/2) x (BN/2).  A tile
 // of the contraction is exactly one block of scales: the instruction takes
-// each lane's row scale as an operand, so the scales cost no arithmetic.  Per
-// tile two steps of 64:
+// each lane's row scale as an operand, so the scales cost no arithmetic.  They
+// are copied to LDS ahead, kPanel blocks at a time, and read from there a tile
+// ahead: read from memory tile by tile, a byte of each of 256 rows, they took
+// as many L2 requests as the operands and 19% of the time (8192 x 6144 x
+// 12288: 575 us, 483 from LDS, 479 with none).  Per tile two steps of 64:
 //   step 0: MFMA | fragment reads of step 1
 //   wait for the next tile's loads, barrier
 //   step 1: MFMA | fragment reads of the next tile | loads of the tile after
 //           next into this tile's buffer
 // ---------------------------------------------------------------------------
+constexpr int kPanel = 124;   // (row stride of 31 words: 32 rows on 32 banks)
+
 template <int BM, int BN, bool GELU>
 __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
   constexpr int NW = 4, WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
   constexpr int A_BYTES = BM * kBK, STAGE = (BM + BN) * kBK;
   constexpr int A_DMA = BM / 32, B_DMA = BN / 32, N_DMA = A_DMA + B_DMA;   // 8 rows per instruction
+  constexpr int B_BLOCKS = BN / 128;
   static_assert(WTN <= 128 && 128 % WTN == 0, "one scale of B per wave");
-  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE + (BM + B_BLOCKS) * kPanel];
+  uint8_t* panel = reinterpret_cast<uint8_t*>(smem + 2 * STAGE);
 
   int tm, tn;
   find_tile(a, tm, tn);
@@ -157,13 +172,48 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
     for (int i = 0; i < 4; ++i) d[4 * e + i] = static_cast<int>(v[i]);
   };
 
-  // Scales: byte of the lane's row per block of A, one byte per wave of B.
-  const uint8_t* sa[FM];
+  // Scales: rows of A's, then the block rows of B's, a thread per row; in
+  // vectors where the rows are aligned to words.
+  const int KT = (a.K + kBK - 1) / kBK;
+  auto fill_panel = [&](int kb0) {
+    const int n = min(KT - kb0, kPanel);
+    for (int row = tid; row < BM + B_BLOCKS; row += 64 * NW) {
+      const bool of_a = row < BM;
+      const uint8_t* src = (of_a ? a.sa + static_cast<int64_t>(min(m0 + row, a.M - 1)) * a.ld_sa
+                                 : a.sb + static_cast<int64_t>(min(n0 + 128 * (row - BM), a.N - 1) / 128) * a.ld_sb) + kb0;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(panel + row * kPanel);
+      constexpr int kVec = kPanel / 16;
+      int done = 0;
+      if (a.scale_words) {
+        u32x4 v[kVec];
 #pragma unroll
-  for (int j = 0; j < FM; ++j)
-    sa[j] = a.sa + static_cast<int64_t>(min(m0 + wm * WTM + 32 * j + r, a.M - 1)) * a.ld_sa;
-  const uint8_t* sb = a.sb + static_cast<int64_t>(min(n0 + wn * WTN, a.N - 1) / 128) * a.ld_sb;
-  int va[FM], vb = 0;
+        for (int c = 0; c < kVec; ++c)
+          if (16 * c + 16 <= n) v[c] = *reinterpret_cast<const u32x4_a4*>(src + 16 * c);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+          if (16 * c + 16 <= n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[4 * c + e] = v[c][e];
+          }
+        done = min(n, 16 * kVec) & ~15;
+      }
+#pragma unroll 8
+      for (int k = done; k < n; ++k) reinterpret_cast<uint8_t*>(dst)[k] = src[k];
+    }
+    wait_loads();   // (here: the compiler would wait in the main loop instead)
+  };
+  const int pa0 = (wm * WTM + r) * kPanel, pb0 = (BM + wn * WTN / 128) * kPanel;
+  int va[FM], vb = 0, na[FM], nb = 0;     // of this tile, of the next
+  auto read_scales = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) na[j] = read_byte((lds_bytes)(panel + pa0 + 32 * j * kPanel + k));
+    nb = read_byte((lds_bytes)(panel + pb0 + k));
+  };
+  auto next_scales = [&] {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) va[j] = na[j];
+    vb = nb;
+  };
 
   f32x16 acc[FN][FM];
 #pragma unroll
@@ -176,24 +226,29 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
   };
 
   constexpr int NMF = FM * FN, NRD = 2 * (FM + FN);
-  const int KT = (a.K + kBK - 1) / kBK;
   if (KT > 0) {
 #pragma unroll
     for (int d = 0; d < N_DMA; ++d) load(0, add_of(0), d);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) va[j] = sa[j][0];
-    vb = sb[0];
+    fill_panel(0);
     wait_loads();
     __syncthreads();
+    read_scales(0);
+    next_scales();
 #pragma unroll
     for (int f = 0; f < NRD; ++f) fread(0, 0, 0, f);
 #pragma unroll
     for (int d = 0; d < N_DMA; ++d) load(1, add_of(kBK), d);
   }
+  int kp = 0;                   // block of the next tile in the panel
   for (int kt = 0; kt < KT; ++kt) {
     const int cur = kt & 1, nxt = cur ^ 1;
-    int na[FM], nb;
-    const int next = min(kt + 1, KT - 1);
+    if (++kp == kPanel) {       // (uniform)
+      kp = 0;
+      __syncthreads();          // every wave has read this tile's scales
+      fill_panel(min(kt + 1, KT - 1));
+      __syncthreads();
+    }
+    read_scales(kp);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < NMF; ++q) {
@@ -201,11 +256,6 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
 #pragma unroll
       for (int f = 0; f < NRD; ++f)
         if (f * NMF / NRD == q) fread(cur, 1, 1, f);
-      if (q == 0) {
-#pragma unroll
-        for (int j = 0; j < FM; ++j) na[j] = sa[j][next];
-        nb = sb[next];
-      }
       __builtin_amdgcn_sched_barrier(0);
     }
     wait_loads();
@@ -223,9 +273,7 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
         if (d * NMF / N_DMA == q) load(cur, add, d);
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int j = 0; j < FM; ++j) va[j] = na[j];
-    vb = nb;
+    next_scales();
   }
   wait_loads();       // (loads past K, which land as zeros)
   __syncthreads();    // every wave's fragment reads are done
@@ -236,6 +284,7 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
   constexpr int ERB = BN * 2, ECR = ERB / 16, ERI = 64 * NW / ECR, EIT = BM / ERI;
   constexpr int ESW = ECR < 32 ? ECR - 1 : 31;
   static_assert(BM * ERB <= 2 * STAGE && 32 % ERI == 0, "staged store");
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     const int lr = wm * WTM + 32 * j + r;
@@ -462,7 +511,8 @@ cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   G8Args a{L.a, L.b, L.sa, L.sb, L.c, static_cast<int>(L.M), static_cast<int>(L.N), static_cast<int>(L.K), 0, 0,
            static_cast<int>(L.lda), static_cast<int>(L.ldb), static_cast<int>(L.ldc), static_cast<int>(L.ld_sa),
-           static_cast<int>(L.ld_sb), L.gelu};
+           static_cast<int>(L.ld_sb), L.gelu,
+           ((reinterpret_cast<uintptr_t>(L.sa) | reinterpret_cast<uintptr_t>(L.sb) | L.ld_sa | L.ld_sb) & 3) == 0};
   auto tiles = [&](int64_t b) { return ((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
   if (tiles(64) > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
   const bool f32 = L.out_t == CCE_F32;

@@ -353,6 +353,8 @@ cce_status cce_block_scaled_gemm(cce_ctx* ctx, cce_dtype out_t, const uint8_t* a
     CCE_TRY(check_ld("a", a_shape.ld));
     CCE_TRY(check_ld("b", b_shape.ld));
     CCE_TRY(check_ld("c", c_shape.ld));
+    CCE_TRY(check_ld("a_scales", ld_a_scales));
+    CCE_TRY(check_ld("b_scales", ld_b_scales));
     CCE_TRY(check_scales("a_scales", a_scales, sam));
     CCE_TRY(check_scales("b_scales", b_scales, sbm));
     CCE_TRY(check_spans({{"a", a, as, false},
