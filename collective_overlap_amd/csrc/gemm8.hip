@@ -36,7 +36,6 @@ typedef const __attribute__((address_space(3))) uint8_t* lds_bytes;
 
 constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x40000000;      // past every buffer below
-constexpr int kNontemporal = 2;            // buffer instruction cache policy
 constexpr int kBK = 128;                   // bytes of the contraction per tile: one scale block
 
 struct G8Args {
@@ -121,6 +120,37 @@ __device__ __forceinline__ void find_tile(const G8Args& a, int& tm, int& tn) {
 // ---------------------------------------------------------------------------
 constexpr int kPanel = 124;   // (row stride of 31 words: 32 rows on 32 banks)
 
+// Copies n blocks' scales from block kb0 on to the panel: BM rows of A's from
+// row m0, then B_BLOCKS block rows of B's from column n0; a thread per row, in
+// vectors where the rows are aligned to words.
+template <int BM, int B_BLOCKS>
+__device__ __forceinline__ void copy_scales(const G8Args& a, uint8_t* panel, int m0, int n0, int kb0, int n) {
+  for (int row = threadIdx.x; row < BM + B_BLOCKS; row += 256) {
+    const uint8_t* src =
+        (row < BM ? a.sa + static_cast<int64_t>(min(m0 + row, a.M - 1)) * a.ld_sa
+                  : a.sb + static_cast<int64_t>(min(n0 + 128 * (row - BM), a.N - 1) / 128) * a.ld_sb) + kb0;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(panel + row * kPanel);
+    constexpr int kVec = kPanel / 16;
+    int done = 0;
+    if (a.scale_words) {
+      u32x4 v[kVec];
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        if (16 * c + 16 <= n) v[c] = *reinterpret_cast<const u32x4_a4*>(src + 16 * c);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        if (16 * c + 16 <= n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[4 * c + e] = v[c][e];
+        }
+      done = min(n, 16 * kVec) & ~15;
+    }
+#pragma unroll 8
+    for (int k = done; k < n; ++k) reinterpret_cast<uint8_t*>(dst)[k] = src[k];
+  }
+  wait_loads();   // (here: the compiler would wait in the main loop instead)
+}
+
 template <int BM, int BN, bool GELU>
 __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
   constexpr int NW = 4, WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
@@ -172,36 +202,8 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
     for (int i = 0; i < 4; ++i) d[4 * e + i] = static_cast<int>(v[i]);
   };
 
-  // Scales: rows of A's, then the block rows of B's, a thread per row; in
-  // vectors where the rows are aligned to words.
   const int KT = (a.K + kBK - 1) / kBK;
-  auto fill_panel = [&](int kb0) {
-    const int n = min(KT - kb0, kPanel);
-    for (int row = tid; row < BM + B_BLOCKS; row += 64 * NW) {
-      const bool of_a = row < BM;
-      const uint8_t* src = (of_a ? a.sa + static_cast<int64_t>(min(m0 + row, a.M - 1)) * a.ld_sa
-                                 : a.sb + static_cast<int64_t>(min(n0 + 128 * (row - BM), a.N - 1) / 128) * a.ld_sb) + kb0;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(panel + row * kPanel);
-      constexpr int kVec = kPanel / 16;
-      int done = 0;
-      if (a.scale_words) {
-        u32x4 v[kVec];
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-          if (16 * c + 16 <= n) v[c] = *reinterpret_cast<const u32x4_a4*>(src + 16 * c);
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-          if (16 * c + 16 <= n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[4 * c + e] = v[c][e];
-          }
-        done = min(n, 16 * kVec) & ~15;
-      }
-#pragma unroll 8
-      for (int k = done; k < n; ++k) reinterpret_cast<uint8_t*>(dst)[k] = src[k];
-    }
-    wait_loads();   // (here: the compiler would wait in the main loop instead)
-  };
+  auto fill_panel = [&](int kb0) { copy_scales<BM, B_BLOCKS>(a, panel, m0, n0, kb0, min(KT - kb0, kPanel)); };
   const int pa0 = (wm * WTM + r) * kPanel, pb0 = (BM + wn * WTN / 128) * kPanel;
   int va[FM], vb = 0, na[FM], nb = 0;     // of this tile, of the next
   auto read_scales = [&](int k) {
@@ -325,90 +327,178 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// 64 x 64 tiles, one block of 128 of the contraction at a time: both operands
-// through LDS as they are, widened to bf16 on the way to the matrix cores.
+// fp32 results, and products too small for the tiles above: e4m3 widened to
+// bf16 between LDS and the matrix cores (v_mfma_f32_32x32x16_bf16), the scale
+// with it.  BM x BN x 128 tiles in the LDS layout of gemm8_kernel, NS stages:
+// the loads of tile kt + NS - 1 go out behind the barrier of tile kt, into the
+// buffer that every wave has left.  A lane's 16-byte chunk feeds two
+// instructions (the order of the k among them is the same for both operands).
 // ---------------------------------------------------------------------------
-template <typename TOut>
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+template <int BM, int BN, int NS, typename TOut>
 __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
-  constexpr int BM = 64, BN = 64, ROW = 128 + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t sha[BM * ROW];
-  __shared__ __attribute__((aligned(16))) uint8_t shb[BN * ROW];
-  const int tm = blockIdx.x / a.tiles_n, tn = blockIdx.x - tm * a.tiles_n;
+  constexpr int NW = 4, WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
+  constexpr int A_BYTES = BM * kBK, STAGE = (BM + BN) * kBK;
+  constexpr int A_DMA = BM / 32, B_DMA = BN / 32, N_DMA = A_DMA + B_DMA;
+  static_assert(BN <= 128, "one scale of B per workgroup");
+  __shared__ __attribute__((aligned(16))) char smem[NS * STAGE + (BM + 1) * kPanel];
+  uint8_t* panel = reinterpret_cast<uint8_t*>(smem + NS * STAGE);
+
+  int tm, tn;
+  find_tile(a, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const __amdgpu_buffer_rsrc_t ra =
+      make_rsrc(a.a + static_cast<int64_t>(m0) * a.lda, static_cast<int64_t>(min(a.M - m0, BM) - 1) * a.lda + a.K);
+  const __amdgpu_buffer_rsrc_t rb =
+      make_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<int64_t>(min(a.N - n0, BN) - 1) * a.ldb + a.K);
+  const int dl_row = 8 * wave + (lane >> 3);
+  const int dl_chunk = (lane & 7) ^ swz(dl_row);
+  const uint32_t off_a = static_cast<uint32_t>(dl_row) * a.lda + 16u * dl_chunk;
+  const uint32_t off_b = static_cast<uint32_t>(dl_row) * a.ldb + 16u * dl_chunk;
+  auto load = [&](int buf, int k0) {
+    const uint32_t add = k0 + (k0 + 16 * dl_chunk < a.K ? 0u : kOob);
+    char* s = smem + buf * STAGE + wave * 1024;
+#pragma unroll
+    for (int d = 0; d < A_DMA; ++d) dma16(ra, s + d * NW * 1024, off_a + add + 32u * d * a.lda);
+#pragma unroll
+    for (int d = 0; d < B_DMA; ++d) dma16(rb, s + A_BYTES + d * NW * 1024, off_b + add + 32u * d * a.ldb);
+  };
+  const int KT = (a.K + kBK - 1) / kBK;
+  auto fill_panel = [&](int kb0) { copy_scales<BM, 1>(a, panel, m0, n0, kb0, min(KT - kb0, kPanel)); };
+
   const int r = lane & 31, h = lane >> 5;
-  f32x16 acc = {};
-  const int m = m0 + wm + r;
-  for (int k0 = 0; k0 < a.K; k0 += 128) {
-    __syncthreads();
+  const int fa0 = (wm * WTM + r) * kBK, fb0 = A_BYTES + (wn * WTN + r) * kBK;
+  const int pa0 = (wm * WTM + r) * kPanel, pb0 = BM * kPanel;
+  f32x16 acc[FN][FM];
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int row = (tid >> 3) + 32 * p, c = (tid & 7) * 16;
-      u32x4 va = {}, vb = {};
-      if (m0 + row < a.M && k0 + c < a.K)
-        va = *reinterpret_cast<const u32x4*>(a.a + static_cast<int64_t>(m0 + row) * a.lda + k0 + c);
-      if (n0 + row < a.N && k0 + c < a.K)
-        vb = *reinterpret_cast<const u32x4*>(a.b + static_cast<int64_t>(n0 + row) * a.ldb + k0 + c);
-      *reinterpret_cast<u32x4*>(sha + row * ROW + c) = va;
-      *reinterpret_cast<u32x4*>(shb + row * ROW + c) = vb;
-    }
-    __syncthreads();
-    const int kb = k0 / 128;
-    const float fa = scale_float(m < a.M ? a.sa[static_cast<int64_t>(m) * a.ld_sa + kb] : 127);
-    const float fb = scale_float(a.sb[static_cast<int64_t>(n0 / 128) * a.ld_sb + kb]);
+  for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int kk = 0; kk < 128; kk += 16) {
-      const u32x2 xa = *reinterpret_cast<const u32x2*>(sha + (wm + r) * ROW + kk + 8 * h);
-      const u32x2 xb = *reinterpret_cast<const u32x2*>(shb + (wn + r) * ROW + kk + 8 * h);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(scaled(xb, fb), scaled(xa, fa), acc, 0, 0, 0);
-    }
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+
+  if (KT > 0) {
+    fill_panel(0);
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d) load(d, d * kBK);
   }
-  // the result block is C^T: the lane holds row m, columns 8 q + 4 h + e
-  if (m >= a.M) return;
-  TOut* c = reinterpret_cast<TOut*>(a.c) + static_cast<int64_t>(m) * a.ldc;
+  int cur = 0, kp = 0;          // buffer of tile kt, its block in the panel
+  for (int kt = 0; kt < KT; ++kt) {
+    wait_vmcnt<(NS - 2) * N_DMA>();
+    if (kp == kPanel) {         // (uniform)
+      kp = 0;
+      __syncthreads();          // every wave has read its last scales
+      fill_panel(kt);
+    }
+    __syncthreads();
+    const int prv = cur == 0 ? NS - 1 : cur - 1;
+    load(prv, (kt + NS - 1) * kBK);
+    float fa[FM], fb = scale_float(read_byte((lds_bytes)(panel + pb0 + kp)));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int n = n0 + wn + 8 * (i / 4) + 4 * h + i % 4;
-    const float v = a.gelu ? gelu_exact(acc[i]) : acc[i];
-    if (n < a.N) c[n] = static_cast<TOut>(v);
+    for (int j = 0; j < FM; ++j) fa[j] = scale_float(read_byte((lds_bytes)(panel + pa0 + 32 * j * kPanel + kp)));
+    const char* s = smem + cur * STAGE;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = ((2 * q + h) ^ swz(r)) << 4;
+      u32x4 xa[FM], xb[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) xb[i] = *reinterpret_cast<const u32x4*>(s + fb0 + 32 * i * kBK + c);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) xa[j] = *reinterpret_cast<const u32x4*>(s + fa0 + 32 * j * kBK + c);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        bf16x8 vb[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) vb[i] = scaled(u32x2{xb[i][2 * e], xb[i][2 * e + 1]}, fb);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+          const bf16x8 va = scaled(u32x2{xa[j][2 * e], xa[j][2 * e + 1]}, fa[j]);
+#pragma unroll
+          for (int i = 0; i < FN; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb[i], va, acc[i][j], 0, 0, 0);
+        }
+      }
+    }
+    ++kp;
+    cur = cur + 1 == NS ? 0 : cur + 1;
+  }
+  wait_loads();       // (loads past K, which land as zeros)
+  // the result block is C^T: the lane holds row m, columns 8 q + 4 h + e
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int m = m0 + wm * WTM + 32 * j + r;
+    if (m >= a.M) continue;
+    TOut* c = reinterpret_cast<TOut*>(a.c) + static_cast<int64_t>(m) * a.ldc;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + wn * WTN + 32 * i + 8 * q + 4 * h;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = a.gelu ? gelu_exact(acc[i][j][4 * q + e]) : acc[i][j][4 * q + e];
+        if (n + 4 <= a.N) {       // (16 or 8 bytes, aligned: ldc is a multiple of 8)
+          if constexpr (sizeof(TOut) == 4) {
+            *reinterpret_cast<f32x4*>(c + n) = f32x4{v[0], v[1], v[2], v[3]};
+          } else {
+            bf16x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = static_cast<__bf16>(v[e]);
+            *reinterpret_cast<bf16x4*>(c + n) = x;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) c[n + e] = static_cast<TOut>(v[e]);
+        }
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 16 FM): the time is that of reading B once.  A workgroup
-// takes 16 columns; its WAVES waves take every WAVES-th block of 128 of the
-// contraction, straight from memory to registers, two blocks ahead, and join
-// their sums through LDS in the order of the waves.  v_mfma_f32_16x16x32_bf16:
-// lane l holds row l & 15 and the 16-byte chunks l / 16 and l / 16 + 4 of a
-// block, so a load instruction reads 64 consecutive bytes of 16 rows; each
-// chunk feeds two instructions of 32 (which k go together is the same for
-// both operands, so their order does not matter).
+// Few rows, and small products: the time is that of reading B once, or of one
+// trip to memory.  A workgroup takes 16 FM rows and 16 FN columns; its WAVES
+// waves take every WAVES-th block of 128 of the contraction, straight from
+// memory to registers, DEPTH blocks ahead, and join their sums through LDS in
+// the order of the waves.  v_mfma_f32_16x16x32_bf16: lane l holds row l & 15
+// and the 16-byte chunks l / 16 and l / 16 + 4 of a block, so a load
+// instruction reads 64 consecutive bytes of 16 rows; each chunk feeds two
+// instructions of 32 (which k go together is the same for both operands, so
+// their order does not matter).
 // ---------------------------------------------------------------------------
-template <int FM, int WAVES, typename TOut>
+template <int FM, int FN, int WAVES, typename TOut>
 __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
-  __shared__ f32x4 part[WAVES > 1 ? WAVES - 1 : 1][FM][64];
+  __shared__ f32x4 part[WAVES > 1 ? WAVES - 1 : 1][FM][FN][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
+  const int tm = blockIdx.x / a.tiles_n, tn = blockIdx.x - tm * a.tiles_n;
+  const int m0 = tm * 16 * FM, n0 = tn * 16 * FN;
   const int KB = (a.K + 127) / 128;
   // Rows past the end and chunks past K are out of the buffers' range: zeros.
   const __amdgpu_buffer_rsrc_t rb =
-      make_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<int64_t>(min(a.N - n0, 16) - 1) * a.ldb + a.K);
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.a, static_cast<int64_t>(a.M - 1) * a.lda + a.K);
-  const uint32_t off_b = n0 + r < a.N ? static_cast<uint32_t>(r) * a.ldb : kOob;
+      make_rsrc(a.b + static_cast<int64_t>(n0) * a.ldb, static_cast<int64_t>(min(a.N - n0, 16 * FN) - 1) * a.ldb + a.K);
+  const __amdgpu_buffer_rsrc_t ra =
+      make_rsrc(a.a + static_cast<int64_t>(m0) * a.lda, static_cast<int64_t>(min(a.M - m0, 16 * FM) - 1) * a.lda + a.K);
   const uint8_t* sb = a.sb + static_cast<int64_t>(n0 / 128) * a.ld_sb;
-  uint32_t off_a[FM];
   const uint8_t* sa[FM];
+  uint32_t off_a[FM], off_b[FN];
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
-    const int m = 16 * j + r;
-    off_a[j] = m < a.M ? static_cast<uint32_t>(m) * a.lda : kOob;
+    const int m = m0 + 16 * j + r;
+    off_a[j] = m < a.M ? static_cast<uint32_t>(16 * j + r) * a.lda : kOob;
     sa[j] = a.sa + static_cast<int64_t>(min(m, a.M - 1)) * a.ld_sa;
   }
+#pragma unroll
+  for (int i = 0; i < FN; ++i) off_b[i] = n0 + 16 * i + r < a.N ? static_cast<uint32_t>(16 * i + r) * a.ldb : kOob;
   struct Block {
-    u32x4 b[2], a[FM][2];
+    u32x4 b[FN][2], a[FM][2];
     uint32_t sb, sa[FM];
   };
   auto load = [&](Block& x, int kb) {
@@ -416,7 +506,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
     for (int c = 0; c < 2; ++c) {
       const int k = kb * 128 + 64 * c + 16 * g;
       const uint32_t add = k + (k < a.K ? 0u : kOob);
-      x.b[c] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b + add, 0, kNontemporal);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) x.b[i][c] = __builtin_amdgcn_raw_buffer_load_b128(rb, off_b[i] + add, 0, 0);
 #pragma unroll
       for (int j = 0; j < FM; ++j) x.a[j][c] = __builtin_amdgcn_raw_buffer_load_b128(ra, off_a[j] + add, 0, 0);
     }
@@ -427,26 +518,31 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
 #pragma unroll
     for (int j = 0; j < FM; ++j) x.sa[j] = sa[j][s];
   };
-  f32x4 acc[FM];
+  f32x4 acc[FM][FN];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) acc[j] = f32x4{};
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int i = 0; i < FN; ++i) acc[j][i] = f32x4{};
   auto use = [&](const Block& x) {
     const float fb = scale_float(x.sb);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bf16x8 vb = scaled(u32x2{x.b[c][2 * e], x.b[c][2 * e + 1]}, fb);
+        bf16x8 vb[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) vb[i] = scaled(u32x2{x.b[i][c][2 * e], x.b[i][c][2 * e + 1]}, fb);
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
           const bf16x8 va = scaled(u32x2{x.a[j][c][2 * e], x.a[j][c][2 * e + 1]}, scale_float(x.sa[j]));
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, va, acc[j], 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < FN; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[i], va, acc[j][i], 0, 0, 0);
         }
       }
     }
   };
   if (wave < KB) {
-    constexpr int DEPTH = FM > 2 ? 2 : 4;      // blocks in flight per wave
+    constexpr int DEPTH = FM + FN > 2 ? 2 : 4;      // blocks in flight per wave
     Block x[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
@@ -464,36 +560,38 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
   }
   if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) part[wave - 1][j][lane] = acc[j];
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i) part[wave - 1][j][i][lane] = acc[j][i];
   }
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
-    for (int w = 0; w < WAVES - 1; ++w) acc[j] = acc[j] + part[w][j][lane];
-    // the result block is C^T: the lane holds row r, columns 4 g + e
-    if (16 * j + r >= a.M) continue;
-    TOut* c = reinterpret_cast<TOut*>(a.c) + static_cast<int64_t>(16 * j + r) * a.ldc;
+    const int m = m0 + 16 * j + r;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int n = n0 + 4 * g + e;
-      const float v = a.gelu ? gelu_exact(acc[j][e]) : acc[j][e];
-      if (n < a.N) c[n] = static_cast<TOut>(v);
+    for (int i = 0; i < FN; ++i) {
+#pragma unroll
+      for (int w = 0; w < WAVES - 1; ++w) acc[j][i] = acc[j][i] + part[w][j][i][lane];
+      if (m >= a.M) continue;
+      // the result block is C^T: the lane holds row r, columns 4 g + e
+      TOut* c = reinterpret_cast<TOut*>(a.c) + static_cast<int64_t>(m) * a.ldc;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = n0 + 16 * i + 4 * g + e;
+        const float v = a.gelu ? gelu_exact(acc[j][i][e]) : acc[j][i][e];
+        if (n < a.N) c[n] = static_cast<TOut>(v);
+      }
     }
   }
 }
 
-template <int FM, int WAVES>
-void launch_rows(const G8Args& a, bool f32, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.N + 15) / 16));
-  if (f32) gemm8_rows_kernel<FM, WAVES, float><<<grid, 64 * WAVES, 0, s>>>(a);
-  else gemm8_rows_kernel<FM, WAVES, __bf16><<<grid, 64 * WAVES, 0, s>>>(a);
-}
-
-template <int FM>
-void launch_rows(const G8Args& a, bool f32, hipStream_t s) {
-  if (a.N > 4096) launch_rows<FM, 4>(a, f32, s);
-  else launch_rows<FM, 8>(a, f32, s);
+template <int FM, int FN, int WAVES>
+void launch_rows(G8Args a, bool f32, hipStream_t s) {
+  a.tiles_n = (a.N + 16 * FN - 1) / (16 * FN);
+  const dim3 grid(static_cast<unsigned>((a.M + 16 * FM - 1) / (16 * FM)) * a.tiles_n);
+  if (f32) gemm8_rows_kernel<FM, FN, WAVES, float><<<grid, 64 * WAVES, 0, s>>>(a);
+  else gemm8_rows_kernel<FM, FN, WAVES, __bf16><<<grid, 64 * WAVES, 0, s>>>(a);
 }
 
 template <int BM, int BN>
@@ -503,6 +601,15 @@ void launch_tiles(G8Args a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.tiles_m) * a.tiles_n);
   if (a.gelu) gemm8_kernel<BM, BN, true><<<grid, 256, 0, s>>>(a);
   else gemm8_kernel<BM, BN, false><<<grid, 256, 0, s>>>(a);
+}
+
+template <int BM, int BN, int NS>
+void launch_wide(G8Args a, bool f32, hipStream_t s) {
+  a.tiles_m = (a.M + BM - 1) / BM;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  const dim3 grid(static_cast<unsigned>(a.tiles_m) * a.tiles_n);
+  if (f32) gemm8_wide_kernel<BM, BN, NS, float><<<grid, 256, 0, s>>>(a);
+  else gemm8_wide_kernel<BM, BN, NS, __bf16><<<grid, 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -516,21 +623,24 @@ cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
   auto tiles = [&](int64_t b) { return ((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
   if (tiles(64) > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
   const bool f32 = L.out_t == CCE_F32;
-  if (L.M <= 16) {
-    launch_rows<1>(a, f32, s);
-  } else if (L.M <= 32) {
-    launch_rows<2>(a, f32, s);
-  } else if (L.M <= 64) {
-    launch_rows<4>(a, f32, s);
+  // Few rows, or so few 64 x 64 tiles that a tile's length in K is the time
+  // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 10 against 15).  Two
+  // waves per workgroup where the columns alone fill the GPU (4 x 12288 x
+  // 6144: 15.4 us against 16.2 with four).
+  // Then the largest tiles that come close to one per compute unit; with fewer
+  // than 96 of the 128 x 128 ones the deeper 64 x 64 ones are faster (1000 x
+  // 1000 x 4096: 18 us against 22; 128 x 12288 x 4096, 96 tiles: 23 against 22).
+  if (L.M <= 16 || tiles(64) <= 32) {
+    if (L.N > 4096) launch_rows<1, 1, 2>(a, f32, s);
+    else launch_rows<1, 1, 4>(a, f32, s);
   } else if (!f32 && tiles(256) >= 256) {
     launch_tiles<256, 256>(a, s);
-  } else if (!f32 && tiles(128) >= 64) {
+  } else if (!f32 && L.M > 64 && tiles(128) >= 96) {
     launch_tiles<128, 128>(a, s);
+  } else if (tiles(128) >= 256) {
+    launch_wide<128, 128, 2>(a, f32, s);
   } else {
-    a.tiles_n = static_cast<int>((L.N + 63) / 64);
-    const dim3 grid(static_cast<unsigned>((L.M + 63) / 64 * a.tiles_n));
-    if (f32) gemm8_wide_kernel<float><<<grid, 256, 0, s>>>(a);
-    else gemm8_wide_kernel<__bf16><<<grid, 256, 0, s>>>(a);
+    launch_wide<64, 64, 4>(a, f32, s);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(CCE_EHIP, std::string("block-scaled GEMM launch: ") + hipGetErrorString(e));
