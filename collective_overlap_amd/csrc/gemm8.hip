@@ -624,7 +624,7 @@ cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
   if (tiles(64) > 0x7fffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
   const bool f32 = L.out_t == CCE_F32;
   // Few rows, or so few 64 x 64 tiles that a tile's length in K is the time
-  // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 10 against 15).  Two
+  // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 13 against 15).  Two
   // waves per workgroup where the columns alone fill the GPU (4 x 12288 x
   // 6144: 15.4 us against 16.2 with four).
   // Then the largest tiles that come close to one per compute unit; with fewer

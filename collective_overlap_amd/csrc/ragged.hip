@@ -20,8 +20,8 @@
 //   column form: LDS rows of one l (BM or BN elements).  A fragment is two
 //     transposing reads (ds_read_b64_tr_b16): 16 lanes read 4 l x 16 columns
 //     and each gets 4 l of its own column.  Chunk c of row l is kept at
-//     c ^ ((l & 3) << 2), so that the 4 rows that 32 lanes read at 64 bytes
-//     each fall on all 64 banks.
+//     c ^ swz_col(l), so that the 4 rows that 32 lanes read at 64 bytes each
+//     fall on all 64 banks.
 // Where l ends: chunks and rows past the end are out of the buffer's range
 // and land as zeros; a last chunk that is partly past the end (row form, l
 // not a multiple of 8) is zeroed in LDS, since what lies behind a row may be
@@ -56,7 +56,8 @@ typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x40000000;      // past every buffer below
 constexpr int kBL = 64;                    // l per tile
-constexpr int kNW = 4;                     // waves
+constexpr int kNW = 4;                     // waves (of a group)
+constexpr int kGroups = 4;                 // groups of waves where tiles are few
 
 struct RArgs {
   const __bf16* x;
@@ -171,14 +172,17 @@ __device__ __forceinline__ bool find_row_tile(const RArgs& a, Tile& t) {
   return true;
 }
 
-// Tiles of every expert's matrix (wgrad), in the same order.
+// Tiles of the experts' matrices (wgrad), expert by expert: a tile's time goes
+// by its expert's rows, so each XCD gets a contiguous eighth of every expert's
+// tiles (an XCD with all of the largest expert's took twice the others' time).
+// false: no tile for this workgroup.
 template <int BM>
-__device__ __forceinline__ void find_matrix_tile(const RArgs& a, Tile& t) {
-  const int w = blockIdx.x, per = gridDim.x / 8;
-  const int id = w < per * 8 ? (w & 7) * per + (w >> 3) : w;
-  const int tiles_i = (a.I + BM - 1) / BM;
-  t.e = id / (tiles_i * a.tiles_j);
-  const int rem = id - t.e * tiles_i * a.tiles_j;
+__device__ __forceinline__ bool find_matrix_tile(const RArgs& a, Tile& t) {
+  const int tiles_i = (a.I + BM - 1) / BM, tiles = tiles_i * a.tiles_j, per = (tiles + 7) / 8;
+  const int w = blockIdx.x;
+  t.e = (w >> 3) / per;
+  const int rem = (w & 7) * per + (w >> 3) - t.e * per;
+  if (rem >= tiles) return false;
   constexpr int kBand = 4;
   const int band = rem / (kBand * a.tiles_j);
   const int in_band = rem - band * kBand * a.tiles_j;
@@ -190,6 +194,7 @@ __device__ __forceinline__ void find_matrix_tile(const RArgs& a, Tile& t) {
   lo = wave_max(lo);
   t.lo = __builtin_amdgcn_readfirstlane(lo);
   t.hi = __builtin_amdgcn_readfirstlane(max(lo, row_number(a, t.e + 1)));
+  return true;
 }
 
 // A transposing read.  (The restrict pointer gives it alias information, as an
@@ -209,7 +214,11 @@ struct Operand {
   static constexpr int kRPI = 64 / kChunks;                   // LDS rows per load instruction
   static constexpr int kLoads = kBytes / (1024 * kNW);        // load instructions per wave
   static constexpr int kFrags = WT / 32;
-  static_assert(!COL || kChunks >= 16, "the swizzle needs 16 chunks");
+  static_assert(!COL || kChunks >= 8, "the swizzle needs 8 chunks");
+
+  // Column form: rows of 256 bytes or more start on the same bank, rows of
+  // 128 on two by turns.
+  __device__ static __forceinline__ int swz_col(int l) { return kChunks >= 16 ? (l & 3) << 2 : ((l >> 1) & 1) << 2; }
 
   const __bf16* base;      // (tile's first row, l = 0)
   int ld, rows, L;
@@ -227,7 +236,7 @@ struct Operand {
 #pragma unroll
     for (int p = 0; p < kLoads; ++p) {
       const int r = kRPI * (kNW * p + wave) + r0;   // LDS row: i, or l
-      off[p] = static_cast<uint32_t>(r) * ld * 2u + 16u * (COL ? c ^ ((r & 3) << 2) : chunk);
+      off[p] = static_cast<uint32_t>(r) * ld * 2u + 16u * (COL ? c ^ swz_col(r) : chunk);
     }
     const int h = lane >> 5;
     if constexpr (COL) {
@@ -237,7 +246,7 @@ struct Operand {
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) {
         const int cc = (wt * WT + 32 * f) / 8 + (byte >> 4);
-        ftr[f] = (8 * h + m) * kRowBytes + ((cc ^ (m << 2)) << 4) + (byte & 15);
+        ftr[f] = (8 * h + m) * kRowBytes + ((cc ^ swz_col(m)) << 4) + (byte & 15);
       }
     } else {
       const int r = lane & 31;
@@ -279,11 +288,27 @@ struct Operand {
   __device__ __forceinline__ void zero_tail(char* lds, int l0) const {
     if constexpr (!COL) {
       const int l = L - l0;                      // in the tile: 0 < l < 64, l % 8 != 0
-      for (int r = threadIdx.x; r < BT; r += 64 * kNW) {
+      for (int r = threadIdx.x & (64 * kNW - 1); r < BT; r += 64 * kNW) {
         __bf16* c = reinterpret_cast<__bf16*>(lds + r * kRowBytes + (((l >> 3) ^ swz(r)) << 4));
         for (int e = l & 7; e < 8; ++e) c[e] = static_cast<__bf16>(0.0f);
       }
     }
+  }
+};
+
+// A tile's operands and result.
+template <bool XC, bool YC, typename TOut>
+struct TileArgs {
+  int I, L;                  // rows (columns, wgrad) of the result, length of the sum
+  const __bf16* x;
+  const __bf16* y;
+  TOut* z;                   // of the expert's first result row
+  __device__ __forceinline__ TileArgs(const RArgs& a, const Tile& t, int i0, int j0) {
+    I = XC ? a.I : t.hi - t.lo;
+    L = XC ? t.hi - t.lo : a.L;
+    x = a.x + t.e * a.xe + (XC ? static_cast<int64_t>(t.lo) * a.ldx + i0 : static_cast<int64_t>(t.lo + i0) * a.ldx);
+    y = a.y + t.e * a.ye + (YC ? static_cast<int64_t>(XC ? t.lo : 0) * a.ldy + j0 : static_cast<int64_t>(j0) * a.ldy);
+    z = reinterpret_cast<TOut*>(a.z) + t.e * a.ze + (XC ? 0 : static_cast<int64_t>(t.lo) * a.ldz);
   }
 };
 
@@ -297,26 +322,19 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
   __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
 
   Tile t;
-  if constexpr (XC) {
-    find_matrix_tile<BM>(a, t);
-  } else {
-    if (!find_row_tile<BM>(a, t)) return;
-  }
+  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, t))) return;
   const int i0 = t.ti * BM, j0 = t.tj * BN;
-  const int I = XC ? a.I : t.hi - t.lo, L = XC ? t.hi - t.lo : a.L;
-  const __bf16* x = a.x + t.e * a.xe + (XC ? static_cast<int64_t>(t.lo) * a.ldx + i0
-                                           : static_cast<int64_t>(t.lo + i0) * a.ldx);
-  const __bf16* y = a.y + t.e * a.ye + (YC ? static_cast<int64_t>(XC ? t.lo : 0) * a.ldy + j0
-                                           : static_cast<int64_t>(j0) * a.ldy);
-  TOut* z = reinterpret_cast<TOut*>(a.z) + t.e * a.ze + (XC ? 0 : static_cast<int64_t>(t.lo) * a.ldz);
+  const TileArgs<XC, YC, TOut> p(a, t, i0, j0);
+  const int I = p.I, L = p.L;
+  TOut* z = p.z;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   OX ox;
   OY oy;
-  ox.init(x, a.ldx, I - i0, L, lane, wave, wm);
-  oy.init(y, a.ldy, a.J - j0, L, lane, wave, wn);
+  ox.init(p.x, a.ldx, I - i0, L, lane, wave, wm);
+  oy.init(p.y, a.ldy, a.J - j0, L, lane, wave, wn);
 
   bf16x8 fx[2][FM], fy[2][FN];
   auto fread = [&](int buf, int kk, int slot, int q) {
@@ -428,11 +446,11 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
   const int e_r = tid / ECR, e_c = tid % ECR;
   const bool whole = i0 + BM <= I && j0 + BN <= a.J;
 #pragma unroll
-  for (int p = 0; p < EP; ++p) {
-    if (p > 0) __syncthreads();
+  for (int pass = 0; pass < EP; ++pass) {
+    if (pass > 0) __syncthreads();
 #pragma unroll
     for (int jj = 0; jj < EJP; ++jj) {
-      const int j = p * EJP + jj;
+      const int j = pass * EJP + jj;
       const int lr = wm * 32 * EJP + jj * 32 + (lane & 31);
       char* srow = smem + lr * ERB;
 #pragma unroll
@@ -458,7 +476,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
     for (int it = 0; it < EIT; ++it) {
       const int lr = ERI * it + e_r;
       const u32x4 raw = *reinterpret_cast<const u32x4*>(smem + lr * ERB + ((e_c ^ (lr & ESW)) << 4));
-      const int i = i0 + ((ERI * it) / (32 * EJP)) * WTM + 32 * (p * EJP + ((ERI * it) / 32) % EJP) + (ERI * it) % 32 + e_r;
+      const int i = i0 + ((ERI * it) / (32 * EJP)) * WTM + 32 * (pass * EJP + ((ERI * it) / 32) % EJP) + (ERI * it) % 32 + e_r;
       const int j = j0 + EPC * e_c;
       TOut* dst = z + static_cast<int64_t>(i) * a.ldz + j;
       if (whole || (i < I && j + EPC <= a.J)) {
@@ -473,30 +491,291 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
   }
 }
 
+// Small products: BM x BN tiles with NS stages, so that more tiles are in
+// flight and a tile of l waits less for its loads: those of the tile NS - 1
+// further go out behind a tile's barrier, into the buffer that every wave has
+// left.  With few tiles and a long l, G groups of 4 waves each take every G-th
+// tile of l with stages of their own, and join their sums through LDS in the
+// order of the groups.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+
+// 4 consecutive columns from j on of a row of J.
+template <typename TOut>
+__device__ __forceinline__ void store4(TOut* row, int j, int J, f32x4 v) {
+  if (j + 4 <= J) {       // (aligned: ld is a multiple of 8)
+    if constexpr (sizeof(TOut) == 4) {
+      *reinterpret_cast<f32x4*>(row + j) = v;
+    } else {
+      bf16x4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = static_cast<__bf16>(v[e]);
+      *reinterpret_cast<bf16x4*>(row + j) = h;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < J) row[j + e] = static_cast<TOut>(v[e]);
+  }
+}
+
+template <int BM, int BN, int NS, int G, bool XC, bool YC, typename TOut>
+__global__ __launch_bounds__(64 * kNW * G) void ragged_small_kernel(RArgs a) {
+  constexpr int WTM = BM / 2, WTN = BN / 2, FM = WTM / 32, FN = WTN / 32;
+  using OX = Operand<BM, WTM, XC>;
+  using OY = Operand<BN, WTN, YC>;
+  constexpr int STAGE = OX::kBytes + OY::kBytes, N_DMA = OX::kLoads + OY::kLoads;
+  __shared__ __attribute__((aligned(16))) char smem[G * NS * STAGE];
+  Tile t;
+  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, t))) return;
+  const int i0 = t.ti * BM, j0 = t.tj * BN;
+  const TileArgs<XC, YC, TOut> p(a, t, i0, j0);
+  const int tid = threadIdx.x & (64 * kNW - 1), lane = tid & 63;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / (64 * kNW));
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  OX ox;
+  OY oy;
+  ox.init(p.x, a.ldx, p.I - i0, p.L, lane, wave, wm);
+  oy.init(p.y, a.ldy, a.J - j0, p.L, lane, wave, wn);
+  const int KT = (p.L + kBL - 1) / kBL;
+  const bool tail = (!XC || !YC) && (p.L & 7) != 0;
+  char* stages = smem + group * NS * STAGE;
+  auto load = [&](int buf, int l0) {
+    const __amdgpu_buffer_rsrc_t rx = ox.rsrc(l0), ry = oy.rsrc(l0);
+    const uint32_t ax = ox.add(l0), ay = oy.add(l0);
+    char* s = stages + buf * STAGE;
+#pragma unroll
+    for (int d = 0; d < OX::kLoads; ++d) ox.load(rx, s, ax, d, wave);
+#pragma unroll
+    for (int d = 0; d < OY::kLoads; ++d) oy.load(ry, s + OX::kBytes, ay, d, wave);
+  };
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = f32x16{};
+  // (every group goes as many rounds: a tile past the end is zeros)
+  if (KT > 0) {
+#pragma unroll
+    for (int d = 0; d < NS - 1; ++d) load(d, (group + d * G) * kBL);
+  }
+  int cur = 0;
+  for (int k0 = 0; k0 < KT; k0 += G) {
+    const int kt = k0 + group;
+    wait_vmcnt<(NS - 2) * N_DMA>();
+    __syncthreads();
+    char* s = stages + cur * STAGE;
+    if (tail && k0 + G >= KT) {
+      if (kt == KT - 1) {
+        ox.zero_tail(s, kt * kBL);
+        oy.zero_tail(s + OX::kBytes, kt * kBL);
+      }
+      __syncthreads();
+    }
+    load(cur == 0 ? NS - 1 : cur - 1, (kt + (NS - 1) * G) * kBL);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      bf16x8 fx[FM], fy[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fy[i] = oy.frag(s + OX::kBytes, kk, i);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fx[j] = ox.frag(s, kk, j);
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fy[i], fx[j], acc[i][j], 0, 0, 0);
+    }
+    cur = cur + 1 == NS ? 0 : cur + 1;
+  }
+  wait_vmcnt<0>();    // (loads past the end, which land as zeros)
+  if constexpr (G > 1) {
+    static_assert(FM == 1 && FN == 1 && (G - 1) * 16 * 256 * 4 <= G * NS * STAGE, "join");
+    f32x4* part = reinterpret_cast<f32x4*>(smem);
+    __syncthreads();  // every wave has left the stages
+    if (group > 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        part[((group - 1) * 4 + q) * 256 + tid] =
+            f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+    }
+    __syncthreads();
+    if (group > 0) return;
+    for (int g = 1; g < G; ++g) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = part[((g - 1) * 4 + q) * 256 + tid];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][0][4 * q + e] += v[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int i = i0 + wm * WTM + 32 * j + (lane & 31);
+    if (i >= p.I) continue;
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        store4(p.z + static_cast<int64_t>(i) * a.ldz, j0 + wn * WTN + 32 * n + 8 * q + 4 * (lane >> 5), a.J,
+               f32x4{acc[n][j][4 * q], acc[n][j][4 * q + 1], acc[n][j][4 * q + 2], acc[n][j][4 * q + 3]});
+  }
+}
+
+// A few rows per expert (forward): the time is that of reading the weights of
+// the experts that have rows.  A workgroup takes 16 FM rows of an expert and
+// 16 columns; its WAVES waves take every WAVES-th 64 of l, straight from
+// memory to registers, DEPTH of them ahead, and join their sums through LDS in
+// the order of the waves.  v_mfma_f32_16x16x32_bf16: lane l holds row l & 15
+// and 8 l from 8 (l / 16) on.
+template <int FM, int WAVES, typename TOut>
+__global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RArgs a) {
+  __shared__ f32x4 part[WAVES - 1][FM][64];
+  Tile t;
+  if (!find_row_tile<16 * FM>(a, t)) return;
+  const int i0 = t.ti * 16 * FM, j0 = t.tj * 16;
+  const TileArgs<false, false, TOut> p(a, t, i0, j0);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int KB = (p.L + 63) / 64;
+  const int rows = min(p.I - i0, 16 * FM), cols = min(a.J - j0, 16);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, (static_cast<int64_t>(rows - 1) * a.ldx + p.L) * 2);
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y, (static_cast<int64_t>(cols - 1) * a.ldy + p.L) * 2);
+  uint32_t off_x[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) off_x[j] = 16 * j + r < rows ? static_cast<uint32_t>(16 * j + r) * a.ldx * 2u : kOob;
+  const uint32_t off_y = r < cols ? static_cast<uint32_t>(r) * a.ldy * 2u : kOob;
+  struct Block {
+    u32x4 y[2], x[FM][2];
+  };
+  auto load = [&](Block& b, int kb) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int l = kb * 64 + 32 * c + 8 * g;
+      const uint32_t add = l * 2u + (l < p.L ? 0u : kOob);
+      b.y[c] = __builtin_amdgcn_raw_buffer_load_b128(ry, off_y + add, 0, 0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) b.x[j][c] = __builtin_amdgcn_raw_buffer_load_b128(rx, off_x[j] + add, 0, 0);
+    }
+  };
+  f32x4 acc[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) acc[j] = f32x4{};
+  const bool tail = (p.L & 7) != 0;
+  // (what the last vector of l holds past the end may be anything)
+  auto clip = [&](u32x4 v, int l) {
+    bf16x8 b = __builtin_bit_cast(bf16x8, v);
+    if (tail) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = l + e < p.L ? b[e] : static_cast<__bf16>(0.0f);
+    }
+    return b;
+  };
+  auto use = [&](const Block& b, int kb) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int l = kb * 64 + 32 * c + 8 * g;
+      const bf16x8 vy = clip(b.y[c], l);
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vy, clip(b.x[j][c], l), acc[j], 0, 0, 0);
+    }
+  };
+  if (wave < KB) {
+    constexpr int DEPTH = 4;
+    Block b[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      load(b[d], wave + d * WAVES);
+      __builtin_amdgcn_sched_barrier(0);   // (in the loop's order, which its waits count on)
+    }
+    for (int kb = wave; kb < KB; kb += DEPTH * WAVES) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        use(b[d], kb + d * WAVES);
+        load(b[d], kb + (d + DEPTH) * WAVES);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) part[wave - 1][j][lane] = acc[j];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+#pragma unroll
+    for (int w = 0; w < WAVES - 1; ++w) acc[j] = acc[j] + part[w][j][lane];
+    // the result block is C^T: the lane holds row r, columns 4 g .. + 3
+    const int i = i0 + 16 * j + r;
+    if (i < p.I) store4(p.z + static_cast<int64_t>(i) * a.ldz, j0 + 4 * g, a.J, acc[j]);
+  }
+}
+
+int64_t most_row_tiles(const RArgs& r, int64_t bm) { return r.T / bm + std::min<int64_t>(r.experts, r.T); }
+
+// Workgroups for `groups` times `tiles_i` rows of tiles, eight per eight tiles.
+hipError_t grid_of(RArgs& r, int64_t groups, int64_t tiles_i, int bn, dim3& grid) {
+  r.tiles_j = (r.J + bn - 1) / bn;
+  const int64_t tiles = (tiles_i * r.tiles_j + 7) / 8 * 8;
+  if (tiles > 0x7ffffff0 || groups * tiles > 0x7ffffff0) return hipErrorInvalidValue;
+  grid = dim3(static_cast<unsigned>(groups * tiles));
+  return hipSuccess;
+}
+
 template <int BM, int BN, bool XC, bool YC>
-hipError_t launch_tiles(RArgs& r, bool f32, int64_t tiles_i, hipStream_t s) {
-  r.tiles_j = (r.J + BN - 1) / BN;
-  const int64_t tiles = tiles_i * r.tiles_j;
-  if (tiles > 0x7ffffff0) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(XC ? tiles : (tiles + 7) / 8 * 8));
-  if (f32) ragged_kernel<BM, BN, XC, YC, float><<<grid, 64 * kNW, 0, s>>>(r);
-  else ragged_kernel<BM, BN, XC, YC, __bf16><<<grid, 64 * kNW, 0, s>>>(r);
+hipError_t launch_tiles(RArgs& r, bool f32, hipStream_t s) {
+  dim3 grid;
+  const int64_t tiles_i = XC ? (r.I + int64_t{BM} - 1) / BM : most_row_tiles(r, BM);
+  if (const hipError_t e = grid_of(r, XC ? r.experts : 1, tiles_i, BN, grid); e != hipSuccess) return e;
+  if constexpr (BM == 64) {
+    // a tile or less per compute unit: four groups of waves each (gradients of
+    // 4000 rows, 128 x 256: 33 -> 23 us; two groups with four stages 26)
+    if (static_cast<int64_t>(grid.x) <= 256) {
+      if (f32) ragged_small_kernel<BM, BN, 2, kGroups, XC, YC, float><<<grid, 64 * kNW * kGroups, 0, s>>>(r);
+      else ragged_small_kernel<BM, BN, 2, kGroups, XC, YC, __bf16><<<grid, 64 * kNW * kGroups, 0, s>>>(r);
+    } else {
+      if (f32) ragged_small_kernel<BM, BN, 4, 1, XC, YC, float><<<grid, 64 * kNW, 0, s>>>(r);
+      else ragged_small_kernel<BM, BN, 4, 1, XC, YC, __bf16><<<grid, 64 * kNW, 0, s>>>(r);
+    }
+  } else {
+    if (f32) ragged_kernel<BM, BN, XC, YC, float><<<grid, 64 * kNW, 0, s>>>(r);
+    else ragged_kernel<BM, BN, XC, YC, __bf16><<<grid, 64 * kNW, 0, s>>>(r);
+  }
   return hipGetLastError();
 }
 
-// 256 x 256 tiles where there are enough of them for the 256 compute units,
-// 128 x 128 tiles otherwise.  The count of row tiles is that of even experts:
-// the host does not know the offsets.
+template <int FM>
+hipError_t launch_rows(RArgs& r, bool f32, hipStream_t s) {
+  dim3 grid;
+  if (const hipError_t e = grid_of(r, 1, most_row_tiles(r, 16 * FM), 16, grid); e != hipSuccess) return e;
+  if (f32) ragged_rows_kernel<FM, 4, float><<<grid, 256, 0, s>>>(r);
+  else ragged_rows_kernel<FM, 4, __bf16><<<grid, 256, 0, s>>>(r);
+  return hipGetLastError();
+}
+
+// The largest tiles that there are enough of for the 256 compute units, and
+// that the experts' rows fill.  The host does not know the offsets: it counts
+// as if the experts were even.
 template <bool XC, bool YC>
 hipError_t launch_form(RArgs& r, bool f32, hipStream_t s) {
-  auto tiles_i = [&](int64_t bm) {      // tile rows there can be
-    return XC ? r.experts * ((r.I + bm - 1) / bm) : r.T / bm + std::min<int64_t>(r.experts, r.T);
+  const int64_t rows = r.T / r.experts;      // of an expert
+  auto tiles = [&](int64_t b) {
+    return r.experts * (((XC ? r.I : rows) + b - 1) / b) * ((r.J + b - 1) / b);
   };
-  auto even = [&](int64_t bm) {
-    return XC ? tiles_i(bm) : r.experts * ((r.T / r.experts + bm - 1) / bm);
-  };
-  if (even(256) * ((r.J + 255) / 256) >= 256) return launch_tiles<256, 256, XC, YC>(r, f32, tiles_i(256), s);
-  return launch_tiles<128, 128, XC, YC>(r, f32, tiles_i(128), s);
+  if constexpr (!XC && !YC) {
+    if (rows <= 4) return launch_rows<1>(r, f32, s);
+  }
+  if (tiles(256) >= 256 && (XC || rows >= 96)) return launch_tiles<256, 256, XC, YC>(r, f32, s);
+  if (tiles(128) >= 128 && (XC || rows >= 48)) return launch_tiles<128, 128, XC, YC>(r, f32, s);
+  return launch_tiles<64, 64, XC, YC>(r, f32, s);
 }
 
 }  // namespace
