@@ -77,7 +77,7 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* base, int j, int n, const f
     w[h] = static_cast<unsigned>(p);
   }
   if (j + 8 <= n) {
-    *reinterpret_cast<u32x2*>(base + j) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(base + j));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
