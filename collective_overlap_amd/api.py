@@ -474,22 +474,32 @@ def cce_fused_allreduce_epilogue(ctx: Context, partials, bias, residual, outs, p
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
-def _shape_is(t, shape, what):
+def _ld(t, shape, dtype, what):
+    """ld of a 2-D tensor of this shape and dtype (None: any) with unit column stride.  (These
+    calls take a few microseconds on the device: one check per tensor, no structures.)"""
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype} here, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    rows, cols = shape
+    if step != 1 and cols > 1:
+        raise ValueError("tensor must have unit column stride")
+    return ld if rows > 1 and cols > 0 else max(cols, ld) if cols > 0 else 0
 
 
-def _vector(t, n, what):
-    _shape_is(t, (n,), what)
+def _vector(t, n, what, dtype=None):
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what} must be {dtype} here, got {t.dtype}")
+    if t.shape != (n,):
+        raise ValueError(f"{what} must have shape {(n,)}, got {tuple(t.shape)}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
 
 
 def _scales(t, rows, cols, block_rows, what):
     """ld of the E8M0 scales of a [rows, cols] matrix in block_rows x 128 blocks."""
-    _dtype_is([t], _E8M0, what)
-    _shape_is(t, (-(-rows // block_rows), -(-cols // 128)), what)
-    return _extent(t)[2]
+    return _ld(t, (-(-rows // block_rows), -(-cols // 128)), _E8M0, what)
 
 
 def _ptr(t):
@@ -502,22 +512,20 @@ def cce_rmsnorm(ctx: Context, x, weight, out, eps: float = 1e-5, residual=None, 
     row.  out: float32, bfloat16, or float8_e4m3fn with scales (float8_e8m0fnu, one per row and
     128 columns).  residual_out, if given, receives r."""
     rows, cols, ld = _extent(x)
-    _dtype_is([residual, residual_out], x.dtype, "the residual")
-    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (out, "out")):
-        if t is not None:
-            _shape_is(t, x.shape, what)
+    shape, dtype = x.shape, x.dtype
+    ld_r = ld if residual is None else _ld(residual, shape, dtype, "the residual")
+    ld_ro = ld if residual_out is None else _ld(residual_out, shape, dtype, "residual_out")
+    ld_o = _ld(out, shape, None, "out")
     _vector(weight, cols, "weight")
-    quantized = out.dtype == _E4M3
+    quantized = out.dtype is _E4M3
     if quantized != (scales is not None):
         raise ValueError("scales go with a float8_e4m3fn output")
     ld_s = _scales(scales, rows, cols, 1, "scales") if quantized else 0
-    _on_device(ctx, [x, weight, out, residual, residual_out, scales])
+    _on_device(ctx, (x, weight, out, residual, residual_out, scales))
     check(lib().cce_rmsnorm(
-        ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), _ptr(residual),
-        ld if residual is None else _extent(residual)[2], _ptr(residual_out),
-        ld if residual_out is None else _extent(residual_out)[2], weight.data_ptr(),
-        _dtype(weight.dtype), float(eps), out.data_ptr(),
-        CCE_E4M3 if quantized else _dtype(out.dtype), _extent(out)[2], _ptr(scales), ld_s, 0,
+        ctx.handle, _dtype(dtype), x.data_ptr(), cce_mat(rows, cols, ld), _ptr(residual), ld_r,
+        _ptr(residual_out), ld_ro, weight.data_ptr(), _dtype(weight.dtype), eps, out.data_ptr(),
+        CCE_E4M3 if quantized else _dtype(out.dtype), ld_o, _ptr(scales), ld_s, 0,
         _stream(stream, out.device)), "cce_rmsnorm")
     return out
 
@@ -535,22 +543,19 @@ def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: f
     """Gradients of cce_rmsnorm for its normalised tensor x (residual_out where a residual was
     added): dx, of both summands, with d_residual added; dweight (float32), if given."""
     rows, cols, ld = _extent(x)
-    _dtype_is([dout, dx, d_residual], x.dtype, "dout, dx and d_residual")
-    for t, what in ((dout, "dout"), (dx, "dx"), (d_residual, "d_residual")):
-        if t is not None:
-            _shape_is(t, x.shape, what)
+    shape, dtype = x.shape, x.dtype
+    ld_d, ld_dx = _ld(dout, shape, dtype, "dout"), _ld(dx, shape, dtype, "dx")
+    ld_r = ld if d_residual is None else _ld(d_residual, shape, dtype, "d_residual")
     _vector(weight, cols, "weight")
     if dweight is not None:
-        _dtype_is([dweight], torch.float32, "dweight")
-        _vector(dweight, cols, "dweight")
-    _on_device(ctx, [x, weight, dout, dx, dweight, d_residual, workspace])
-    ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(x.shape), dx.device, workspace,
+        _vector(dweight, cols, "dweight", torch.float32)
+    _on_device(ctx, (x, weight, dout, dx, dweight, d_residual, workspace))
+    ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(shape), dx.device, workspace,
                          stream)
     check(lib().cce_rmsnorm_backward(
-        ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), weight.data_ptr(),
-        _dtype(weight.dtype), dout.data_ptr(), _extent(dout)[2], _ptr(d_residual),
-        ld if d_residual is None else _extent(d_residual)[2], float(eps), dx.data_ptr(),
-        _extent(dx)[2], _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
+        ctx.handle, _dtype(dtype), x.data_ptr(), cce_mat(rows, cols, ld), weight.data_ptr(),
+        _dtype(weight.dtype), dout.data_ptr(), ld_d, _ptr(d_residual), ld_r, eps, dx.data_ptr(),
+        ld_dx, _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
         "cce_rmsnorm_backward")
     return dx
 
@@ -559,15 +564,15 @@ def cce_quantize_blocks(ctx: Context, x, q, scales, block_rows: int = 1, stream=
     """q (float8_e4m3fn) and scales (float8_e8m0fnu) of x in blocks of block_rows x 128:
     block_rows 1 for left operands, 128 for right operands of cce_block_scaled_gemm."""
     rows, cols, ld = _extent(x)
-    _dtype_is([q], _E4M3, "q")
-    _shape_is(q, x.shape, "q")
+    ld_q = _ld(q, x.shape, _E4M3, "q")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     ld_s = _scales(scales, rows, cols, block_rows, "scales")
-    _on_device(ctx, [x, q, scales])
+    _on_device(ctx, (x, q, scales))
     check(lib().cce_quantize_blocks(
         ctx.handle, _dtype(x.dtype), x.data_ptr(), cce_mat(rows, cols, ld), block_rows,
-        q.data_ptr(), _extent(q)[2], scales.data_ptr(), ld_s, 0, _stream(stream, q.device)), "cce_quantize_blocks")
+        q.data_ptr(), ld_q, scales.data_ptr(), ld_s, 0, _stream(stream, q.device)),
+        "cce_quantize_blocks")
     return q
 
 
@@ -575,11 +580,13 @@ def cce_block_scaled_gemm(ctx: Context, a, a_scales, b, b_scales, c, gelu: bool 
                           stream=None):
     """c = a @ b^T over float8_e4m3fn operands: a [M, K] with a scale per row and 128 columns,
     b [N, K] with a scale per 128 x 128 block."""
-    am, bm, cm = _mat(a), _mat(b), _mat(c)
-    _dtype_is([a, b], _E4M3, "a and b")
-    ld_sa = _scales(a_scales, am.rows, am.cols, 1, "a_scales")
-    ld_sb = _scales(b_scales, bm.rows, bm.cols, 128, "b_scales")
-    _on_device(ctx, [a, a_scales, b, b_scales, c])
+    if a.dtype is not _E4M3 or b.dtype is not _E4M3:
+        raise ValueError(f"a and b must be {_E4M3} here, got {a.dtype} and {b.dtype}")
+    ea, eb, cm = _extent(a), _extent(b), _mat(c)
+    am, bm = cce_mat(*ea), cce_mat(*eb)
+    ld_sa = _scales(a_scales, ea[0], ea[1], 1, "a_scales")
+    ld_sb = _scales(b_scales, eb[0], eb[1], 128, "b_scales")
+    _on_device(ctx, (a, a_scales, b, b_scales, c))
     check(lib().cce_block_scaled_gemm(
         ctx.handle, _dtype(c.dtype), a.data_ptr(), am, a_scales.data_ptr(), ld_sa, b.data_ptr(),
         bm, b_scales.data_ptr(), ld_sb, c.data_ptr(), cm, CCE_FLAG_GELU if gelu else 0,
@@ -600,8 +607,7 @@ def _experts(b, what):
 
 
 def _offsets(offsets, experts):
-    _dtype_is([offsets], torch.int64, "offsets")
-    _vector(offsets, experts + 1, "offsets")
+    _vector(offsets, experts + 1, "offsets", torch.int64)
 
 
 def cce_ragged_gemm(ctx: Context, a, b, offsets, c, stream=None):
