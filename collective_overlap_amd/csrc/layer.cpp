@@ -64,6 +64,12 @@ int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
 // Tiles of a product are addressed by 32-bit offsets from their first row.
 constexpr int64_t kMaxLd = int64_t{1} << 20;
 
+constexpr int64_t kMaxRows = int64_t{1} << 30;
+cce_status check_rows(const cce_mat& m) {
+  if (m.rows > kMaxRows) return fail(CCE_EUNSUPPORTED, "more than 2^30 rows");
+  return CCE_OK;
+}
+
 cce_status check_ld(const char* name, int64_t ld) {
   if (ld > kMaxLd) return fail(CCE_EUNSUPPORTED, std::string(name) + ": ld exceeds 2^20 elements");
   return CCE_OK;
@@ -110,6 +116,7 @@ cce_status ragged(int kind, const RaggedArgs& g) {
   CCE_TRY(check_operand("a", g.a, g.a_shape, as));
   CCE_TRY(check_operand("b", g.b, g.b_shape, b1));
   CCE_TRY(check_operand("c", g.c, g.c_shape, cs));
+  CCE_TRY(check_rows(g.a_shape));
   CCE_TRY(check_ld("a", g.a_shape.ld));
   CCE_TRY(check_ld("b", g.b_shape.ld));
   CCE_TRY(check_ld("c", g.c_shape.ld));
@@ -185,6 +192,7 @@ cce_status cce_rmsnorm(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_mat x_sha
                   os = span_bytes(om, q ? 1 : esize(out_t)), ss = q ? span_bytes(sm, 1) : 0,
                   ws = cols * static_cast<int64_t>(esize(weight_t));
     CCE_TRY(check_operand("x", x, x_shape, xs));
+    CCE_TRY(check_rows(x_shape));
     if (residual) CCE_TRY(check_operand("residual", residual, rm, rs));
     if (residual_out) CCE_TRY(check_operand("residual_out", residual_out, rom, ros));
     CCE_TRY(check_operand("out", out, om, os));
@@ -252,6 +260,7 @@ cce_status cce_rmsnorm_backward(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_
                   rs = d_residual ? span_bytes(rm, ex) : 0, os = span_bytes(om, ex),
                   ws = cols * static_cast<int64_t>(esize(weight_t)), dws = dweight ? cols * 4 : 0;
     CCE_TRY(check_operand("x", x, x_shape, xs));
+    CCE_TRY(check_rows(x_shape));
     CCE_TRY(check_ptr("weight", weight, ws));
     CCE_TRY(check_operand("dout", dout, dm, ds));
     if (d_residual) CCE_TRY(check_operand("d_residual", d_residual, rm, rs));
@@ -307,6 +316,7 @@ cce_status cce_quantize_blocks(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_m
     const cce_mat qm{rows, cols, ld_q}, sm{(rows + block_rows - 1) / block_rows, blocks_of(cols), ld_scales};
     const int64_t xs = span_bytes(x_shape, esize(x_t)), qs = span_bytes(qm, 1), ss = span_bytes(sm, 1);
     CCE_TRY(check_operand("x", x, x_shape, xs));
+    CCE_TRY(check_rows(x_shape));
     CCE_TRY(check_operand("q", q, qm, qs));
     CCE_TRY(check_scales("scales", scales, sm));
     CCE_TRY(check_spans({{"x", x, xs, false}, {"q", q, qs, true}, {"scales", scales, ss, true}}));
@@ -350,6 +360,8 @@ cce_status cce_block_scaled_gemm(cce_ctx* ctx, cce_dtype out_t, const uint8_t* a
     if (c_shape.rows != M || c_shape.cols != N) return fail(CCE_EINVAL, "c must be [a rows, b rows]");
     if (K % 16 != 0 || a_shape.ld % 16 != 0 || b_shape.ld % 16 != 0)
       return fail(CCE_EUNSUPPORTED, "the contraction length and both ld must be multiples of 16");
+    CCE_TRY(check_rows(a_shape));
+    CCE_TRY(check_rows(b_shape));
     CCE_TRY(check_ld("a", a_shape.ld));
     CCE_TRY(check_ld("b", b_shape.ld));
     CCE_TRY(check_ld("c", c_shape.ld));

@@ -36,6 +36,7 @@ struct NArgs {
   int64_t ld_x, ld_res, ld_res_out, ld_out, ld_scales;
   float eps;
   bool w_f32;
+  int64_t row0;      // first row of the launch
 };
 
 // Sum over the WAVES waves of a row, the same in every thread.  The threads'
@@ -181,9 +182,9 @@ template <typename TX, typename TW, typename TO, int RPW, int NV>
 __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NArgs a) {
   constexpr int TPR = kThreads / RPW;
   __shared__ double sh[kThreads / 64];
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-  if (row >= a.rows) return;      // (rows of a workgroup only share it where each is one wave)
   const int t = threadIdx.x % TPR;
+  const int64_t row = a.row0 + static_cast<int64_t>(blockIdx.x) * RPW + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  if (row >= a.rows) return;      // (rows of a workgroup only share it where each is one wave)
   const __amdgpu_buffer_rsrc_t rx = row_rsrc<TX>(a.x, row, a.ld_x, a.cols);
   const __amdgpu_buffer_rsrc_t rw = row_rsrc<TW>(a.w, 0, 0, a.cols);
   Raw<TX> x[NV], r[NV];
@@ -230,21 +231,22 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_wide_kernel(NArgs a) {
   __shared__ double sh[kThreads / 64];
   const int tid = threadIdx.x;
   const int vectors = (a.cols + 7) >> 3;
-  const int64_t row = blockIdx.x;
-  float ss = 0.0f;
-  for (int i = tid; i < vectors; i += kThreads) {
-    float v[8];
-    load_sum<TX>(a, row, 8 * i, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-    if (a.res_out) store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, 8 * i, a.cols, v);
-  }
-  const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
-  for (int i0 = 0; i0 < vectors; i0 += kThreads) {   // (every lane: a scale's maximum needs its 16)
-    float v[8], w[8];
-    load_sum<TX>(a, row, 8 * (i0 + tid), v);
-    load_weight(a, 8 * (i0 + tid), w);
-    finish<TO>(a, row, i0 + tid, v, w, rstd);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float ss = 0.0f;
+    for (int i = tid; i < vectors; i += kThreads) {
+      float v[8];
+      load_sum<TX>(a, row, 8 * i, v);
+  #pragma unroll
+      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+      if (a.res_out) store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, 8 * i, a.cols, v);
+    }
+    const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
+    for (int i0 = 0; i0 < vectors; i0 += kThreads) {   // (every lane: a scale's maximum needs its 16)
+      float v[8], w[8];
+      load_sum<TX>(a, row, 8 * (i0 + tid), v);
+      load_weight(a, 8 * (i0 + tid), w);
+      finish<TO>(a, row, i0 + tid, v, w, rstd);
+    }
   }
 }
 
@@ -377,38 +379,39 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
   wa.w = a.w;
   wa.cols = a.cols;
   wa.w_f32 = a.w_f32;
-  const int64_t row = blockIdx.x;
-  const TX* x = reinterpret_cast<const TX*>(a.x) + row * a.ld_x;
-  const TX* dy = reinterpret_cast<const TX*>(a.dout) + row * a.ld_dout;
-  float ss = 0.0f, dot = 0.0f;
-  for (int i = tid; i < vectors; i += kThreads) {
-    float v[8], d[8], w[8];
-    load8(x, 8 * i, a.cols, v);
-    load8(dy, 8 * i, a.cols, d);
-    load_weight(wa, 8 * i, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ss += v[e] * v[e];
-      dot += d[e] * w[e] * v[e];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const TX* x = reinterpret_cast<const TX*>(a.x) + row * a.ld_x;
+    const TX* dy = reinterpret_cast<const TX*>(a.dout) + row * a.ld_dout;
+    float ss = 0.0f, dot = 0.0f;
+    for (int i = tid; i < vectors; i += kThreads) {
+      float v[8], d[8], w[8];
+      load8(x, 8 * i, a.cols, v);
+      load8(dy, 8 * i, a.cols, d);
+      load_weight(wa, 8 * i, w);
+  #pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss += v[e] * v[e];
+        dot += d[e] * w[e] * v[e];
+      }
     }
-  }
-  const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
-  const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) / a.cols) * rstd;
-  if (tid == 0) a.rstd[row] = rstd;
-  for (int i = tid; i < vectors; i += kThreads) {
-    float v[8], d[8], w[8], g[8];
-    load8(x, 8 * i, a.cols, v);
-    load8(dy, 8 * i, a.cols, d);
-    load_weight(wa, 8 * i, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = (d[e] * w[e] - v[e] * rstd * mean) * rstd;
-    if (a.dres) {
-      float r[8];
-      load8(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, 8 * i, a.cols, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] += r[e];
+    const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
+    const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) / a.cols) * rstd;
+    if (tid == 0) a.rstd[row] = rstd;
+    for (int i = tid; i < vectors; i += kThreads) {
+      float v[8], d[8], w[8], g[8];
+      load8(x, 8 * i, a.cols, v);
+      load8(dy, 8 * i, a.cols, d);
+      load_weight(wa, 8 * i, w);
+  #pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = (d[e] * w[e] - v[e] * rstd * mean) * rstd;
+      if (a.dres) {
+        float r[8];
+        load8(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, 8 * i, a.cols, r);
+  #pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] += r[e];
+      }
+      store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, 8 * i, a.cols, g);
     }
-    store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, 8 * i, a.cols, g);
   }
 }
 
@@ -480,33 +483,36 @@ template <typename TX, int TPR>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QArgs a) {
   constexpr int RPW = kThreads / TPR;
   const int chunks = (a.cols + 8 * TPR - 1) / (8 * TPR);
-  const int group = blockIdx.x / chunks, chunk = blockIdx.x - group * chunks;
-  const int j = chunk * 8 * TPR + 8 * (threadIdx.x % TPR);
-  const int64_t row0 = static_cast<int64_t>(group) * RPW * kRowsEach + threadIdx.x / TPR;
-  float v[kRowsEach][8];
+  const int64_t total = (a.rows + int64_t{RPW} * kRowsEach - 1) / (RPW * kRowsEach) * chunks;
+  for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {   // (more than once only in a grid of the most workgroups)
+    const int group = static_cast<int>(b / chunks), chunk = static_cast<int>(b - static_cast<int64_t>(group) * chunks);
+    const int j = chunk * 8 * TPR + 8 * (threadIdx.x % TPR);
+    const int64_t row0 = static_cast<int64_t>(group) * RPW * kRowsEach + threadIdx.x / TPR;
+    float v[kRowsEach][8];
 #pragma unroll
-  for (int u = 0; u < kRowsEach; ++u) {
-    const int64_t row = row0 + u * RPW;
-    if (row < a.rows) {
-      load8<TX, true>(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, v[u]);
-    } else {
+    for (int u = 0; u < kRowsEach; ++u) {
+      const int64_t row = row0 + u * RPW;
+      if (row < a.rows) {
+        load8<TX, true>(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, v[u]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+      }
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kRowsEach; ++u) {
-    const int64_t row = row0 + u * RPW;
-    uint32_t top = 0;
+    for (int u = 0; u < kRowsEach; ++u) {
+      const int64_t row = row0 + u * RPW;
+      uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[u][e]));
-    const uint32_t s = scale_of(max16(top));
-    const float inv = inverse_of(s);
+      for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[u][e]));
+      const uint32_t s = scale_of(max16(top));
+      const float inv = inverse_of(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[u][e] *= inv;
-    if (row < a.rows && j < a.cols) {
-      store8_e4m3(a.q + row * a.ld_q, j, a.cols, v[u]);
-      if ((j & (kScaleCols - 1)) == 0) a.scales[row * a.ld_scales + j / kScaleCols] = static_cast<uint8_t>(s);
+      for (int e = 0; e < 8; ++e) v[u][e] *= inv;
+      if (row < a.rows && j < a.cols) {
+        store8_e4m3(a.q + row * a.ld_q, j, a.cols, v[u]);
+        if ((j & (kScaleCols - 1)) == 0) a.scales[row * a.ld_scales + j / kScaleCols] = static_cast<uint8_t>(s);
+      }
     }
   }
 }
@@ -561,6 +567,10 @@ cce_status launched(const char* what) {
   return CCE_OK;
 }
 
+// A launch has fewer than 2^32 threads: more rows than that take turns.
+constexpr int64_t kMaxGrid = 1 << 22;
+dim3 grid_for(int64_t workgroups) { return dim3(static_cast<unsigned>(std::min(workgroups, kMaxGrid))); }
+
 // Widest row that the kernels keep in registers (two tensors of it in the
 // backward pass; a fourth vector per thread spills there).
 constexpr int64_t kMaxForwardCols = 16384, kMaxBackwardCols = 12288;
@@ -581,10 +591,13 @@ int dweight_lines(int64_t rows, int64_t cols) {
 }
 
 template <typename TX, typename TW, typename TO>
-void launch_norm(const NArgs& a, hipStream_t s) {
+void launch_norm(NArgs a, hipStream_t s) {
   auto go = [&](auto rpw, auto nv) {
     constexpr int RPW = decltype(rpw)::value, NV = decltype(nv)::value;
-    rmsnorm_kernel<TX, TW, TO, RPW, NV><<<dim3((a.rows + RPW - 1) / RPW), kThreads, 0, s>>>(a);
+    // (more than one launch from 2^22 workgroups on: a loop in the kernel made
+    // all calls 6% slower)
+    for (a.row0 = 0; a.row0 < a.rows; a.row0 += kMaxGrid * RPW)
+      rmsnorm_kernel<TX, TW, TO, RPW, NV><<<grid_for((a.rows - a.row0 + RPW - 1) / RPW), kThreads, 0, s>>>(a);
   };
   // A wave per row up to 1024 columns, a workgroup of four per row above.
   if (a.cols <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
@@ -595,7 +608,7 @@ void launch_norm(const NArgs& a, hipStream_t s) {
   else if (a.cols <= 8192) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
   else if (a.cols <= 12288) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 6>{});
   else if (a.cols <= kMaxForwardCols) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
-  else rmsnorm_wide_kernel<TX, TO><<<dim3(a.rows), kThreads, 0, s>>>(a);
+  else rmsnorm_wide_kernel<TX, TO><<<grid_for(a.rows), kThreads, 0, s>>>(a);
 }
 
 template <typename TX, typename TO>
@@ -630,7 +643,7 @@ void launch_backward(const BArgs& a, hipStream_t s) {
 cce_status launch_rmsnorm(const NormLaunch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   NArgs a{L.x, L.res, L.res_out, L.w, L.out, L.scales, static_cast<int>(L.rows), static_cast<int>(L.cols),
-          L.ld_x, L.ld_res, L.ld_res_out, L.ld_out, L.ld_scales, L.eps, L.w_t == CCE_F32};
+          L.ld_x, L.ld_res, L.ld_res_out, L.ld_out, L.ld_scales, L.eps, L.w_t == CCE_F32, 0};
   if (L.x_t == CCE_F32) {
     if (L.out_t == CCE_E4M3) launch_norm_w<float, e4m3>(a, s);
     else if (L.out_t == CCE_F32) launch_norm_w<float, float>(a, s);
@@ -670,8 +683,8 @@ cce_status launch_rmsnorm_backward(const NormBackwardLaunch& L, void* stream) {
   const bool xf = L.x_t == CCE_F32, wide = L.cols > kMaxBackwardCols;
   if (L.rows > 0) {
     if (wide) {
-      if (xf) rmsnorm_backward_wide_kernel<float><<<dim3(a.rows), kThreads, 0, s>>>(a);
-      else rmsnorm_backward_wide_kernel<__bf16><<<dim3(a.rows), kThreads, 0, s>>>(a);
+      if (xf) rmsnorm_backward_wide_kernel<float><<<grid_for(a.rows), kThreads, 0, s>>>(a);
+      else rmsnorm_backward_wide_kernel<__bf16><<<grid_for(a.rows), kThreads, 0, s>>>(a);
     } else if (xf) {
       if (a.w_f32) launch_backward<float, float>(a, s);
       else launch_backward<float, __bf16>(a, s);
@@ -703,7 +716,7 @@ void launch_quantize(const QArgs& a, int block_rows, hipStream_t s) {
   auto go = [&](auto tpr) {
     constexpr int64_t TPR = decltype(tpr)::value, rows = kThreads / TPR * kRowsEach;
     const int64_t groups = ((a.rows + rows - 1) / rows) * ((a.cols + 8 * TPR - 1) / (8 * TPR));
-    quantize_rows_kernel<TX, TPR><<<dim3(static_cast<unsigned>(groups)), kThreads, 0, s>>>(a);
+    quantize_rows_kernel<TX, TPR><<<grid_for(groups), kThreads, 0, s>>>(a);
   };
   // Threads side by side: no more than a row fills.
   if (a.cols <= 256) go(std::integral_constant<int, 16>{});

@@ -57,6 +57,8 @@ constexpr int kBufferFlags = 0x00020000;   // raw buffer, 32-bit data format
 constexpr uint32_t kOob = 0x40000000;      // past every buffer below
 constexpr int kBL = 64;                    // l per tile
 constexpr int kNW = 4;                     // waves (of a group)
+constexpr int kRowWaves = 2;               // waves of a workgroup of ragged_rows_kernel,
+constexpr unsigned kRowGroups = 2048;      // and the most workgroups (4 waves, 1024: 3% slower)
 constexpr int kGroups = 4;                 // groups of waves where tiles are few
 
 struct RArgs {
@@ -139,29 +141,38 @@ __device__ __forceinline__ int scan_experts(const RArgs& a, F&& f) {
 // walks an expert's tiles in bands of 4 tile rows, so that the tiles in
 // flight share X and Y in the XCD's L2.  false: no tile for this workgroup.
 template <int BM>
-__device__ __forceinline__ bool find_row_tile(const RArgs& a, Tile& t) {
-  const int rows = __builtin_amdgcn_readfirstlane(scan_experts<BM>(a, [](int, int, int, int, int) {}));
+__device__ __forceinline__ bool find_row_tile(const RArgs& a, int w, Tile& t) {
+  // Of up to 64 experts the lanes keep what the scan saw; of more, a second
+  // scan finds the tile's.
+  int f = 0, n = 0, lo = 0, hi = 0;
+  const int rows = __builtin_amdgcn_readfirstlane(scan_experts<BM>(a, [&](int f_, int n_, int, int l_, int h_) {
+    f = f_;
+    n = n_;
+    lo = l_;
+    hi = h_;
+  }));
   const int64_t tiles = static_cast<int64_t>(rows) * a.tiles_j;
   const int64_t per = (tiles + 7) / 8;
-  const int w = blockIdx.x;
   const int64_t id = (w & 7) * per + (w >> 3);
   if ((w >> 3) >= per || id >= tiles) return false;
-  int first = 0, mine = 0, e = 0, lo = 0, hi = 0;
-  scan_experts<BM>(a, [&](int f, int n, int ex, int l, int h) {
-    const uint64_t found = __ballot(n > 0 && static_cast<int64_t>(f) * a.tiles_j <= id &&
-                                    id < static_cast<int64_t>(f + n) * a.tiles_j);
+  const int row = __builtin_amdgcn_readfirstlane(static_cast<int>(id / a.tiles_j));    // tile row
+  int first = 0, mine = 0, e = 0, l = 0, h = 0;
+  auto take = [&](int f_, int n_, int e_, int l_, int h_) {
+    const uint64_t found = __ballot(f_ <= row && row < f_ + n_);
     if (found) {
       const int src = __ffsll(static_cast<unsigned long long>(found)) - 1;
-      first = __shfl(f, src);
-      mine = __shfl(n, src);
-      e = __shfl(ex, src);
-      lo = __shfl(l, src);
-      hi = __shfl(h, src);
+      first = __shfl(f_, src);
+      mine = __shfl(n_, src);
+      e = __shfl(e_, src);
+      l = __shfl(l_, src);
+      h = __shfl(h_, src);
     }
-  });
+  };
+  if (a.experts <= 64) take(f, n, threadIdx.x & 63, lo, hi);
+  else scan_experts<BM>(a, take);
   t.e = __builtin_amdgcn_readfirstlane(e);
-  t.lo = __builtin_amdgcn_readfirstlane(lo);
-  t.hi = __builtin_amdgcn_readfirstlane(hi);
+  t.lo = __builtin_amdgcn_readfirstlane(l);
+  t.hi = __builtin_amdgcn_readfirstlane(h);
   const int rem = static_cast<int>(id - static_cast<int64_t>(first) * a.tiles_j);
   constexpr int kBand = 4;
   const int band = rem / (kBand * a.tiles_j);
@@ -306,7 +317,7 @@ struct TileArgs {
   __device__ __forceinline__ TileArgs(const RArgs& a, const Tile& t, int i0, int j0) {
     I = XC ? a.I : t.hi - t.lo;
     L = XC ? t.hi - t.lo : a.L;
-    x = a.x + t.e * a.xe + (XC ? static_cast<int64_t>(t.lo) * a.ldx + i0 : static_cast<int64_t>(t.lo + i0) * a.ldx);
+    x = a.x + t.e * a.xe + (XC ? static_cast<int64_t>(t.lo) * a.ldx + i0 : (static_cast<int64_t>(t.lo) + i0) * a.ldx);
     y = a.y + t.e * a.ye + (YC ? static_cast<int64_t>(XC ? t.lo : 0) * a.ldy + j0 : static_cast<int64_t>(j0) * a.ldy);
     z = reinterpret_cast<TOut*>(a.z) + t.e * a.ze + (XC ? 0 : static_cast<int64_t>(t.lo) * a.ldz);
   }
@@ -322,7 +333,7 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
   __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
 
   Tile t;
-  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, t))) return;
+  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, blockIdx.x, t))) return;
   const int i0 = t.ti * BM, j0 = t.tj * BN;
   const TileArgs<XC, YC, TOut> p(a, t, i0, j0);
   const int I = p.I, L = p.L;
@@ -530,7 +541,7 @@ __global__ __launch_bounds__(64 * kNW * G) void ragged_small_kernel(RArgs a) {
   constexpr int STAGE = OX::kBytes + OY::kBytes, N_DMA = OX::kLoads + OY::kLoads;
   __shared__ __attribute__((aligned(16))) char smem[G * NS * STAGE];
   Tile t;
-  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, t))) return;
+  if (!(XC ? find_matrix_tile<BM>(a, t) : find_row_tile<BM>(a, blockIdx.x, t))) return;
   const int i0 = t.ti * BM, j0 = t.tj * BN;
   const TileArgs<XC, YC, TOut> p(a, t, i0, j0);
   const int tid = threadIdx.x & (64 * kNW - 1), lane = tid & 63;
@@ -635,97 +646,104 @@ __global__ __launch_bounds__(64 * kNW * G) void ragged_small_kernel(RArgs a) {
 template <int FM, int WAVES, typename TOut>
 __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RArgs a) {
   __shared__ f32x4 part[WAVES - 1][FM][64];
+  // (a workgroup takes several tiles, and most tiles that there could be are not
+  // there: a workgroup for each of those took 2 to 3 us of 17)
   Tile t;
-  if (!find_row_tile<16 * FM>(a, t)) return;
-  const int i0 = t.ti * 16 * FM, j0 = t.tj * 16;
-  const TileArgs<false, false, TOut> p(a, t, i0, j0);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int KB = (p.L + 63) / 64;
-  const int rows = min(p.I - i0, 16 * FM), cols = min(a.J - j0, 16);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, (static_cast<int64_t>(rows - 1) * a.ldx + p.L) * 2);
-  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y, (static_cast<int64_t>(cols - 1) * a.ldy + p.L) * 2);
-  uint32_t off_x[FM];
+  for (int w = blockIdx.x; find_row_tile<16 * FM>(a, w, t); w += gridDim.x) {
+    if (w != static_cast<int>(blockIdx.x)) __syncthreads();   // the last tile's sums are read
+    const int i0 = t.ti * 16 * FM, j0 = t.tj * 16;
+    const TileArgs<false, false, TOut> p(a, t, i0, j0);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int KB = (p.L + 63) / 64;
+    const int rows = min(p.I - i0, 16 * FM), cols = min(a.J - j0, 16);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, (static_cast<int64_t>(rows - 1) * a.ldx + p.L) * 2);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y, (static_cast<int64_t>(cols - 1) * a.ldy + p.L) * 2);
+    uint32_t off_x[FM];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) off_x[j] = 16 * j + r < rows ? static_cast<uint32_t>(16 * j + r) * a.ldx * 2u : kOob;
-  const uint32_t off_y = r < cols ? static_cast<uint32_t>(r) * a.ldy * 2u : kOob;
-  struct Block {
-    u32x4 y[2], x[FM][2];
-  };
-  auto load = [&](Block& b, int kb) {
+    for (int j = 0; j < FM; ++j) off_x[j] = 16 * j + r < rows ? static_cast<uint32_t>(16 * j + r) * a.ldx * 2u : kOob;
+    const uint32_t off_y = r < cols ? static_cast<uint32_t>(r) * a.ldy * 2u : kOob;
+    struct Block {
+      u32x4 y[2], x[FM][2];
+    };
+    auto load = [&](Block& b, int kb) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int l = kb * 64 + 32 * c + 8 * g;
-      const uint32_t add = l * 2u + (l < p.L ? 0u : kOob);
-      b.y[c] = __builtin_amdgcn_raw_buffer_load_b128(ry, off_y + add, 0, 0);
+      for (int c = 0; c < 2; ++c) {
+        const int l = kb * 64 + 32 * c + 8 * g;
+        const uint32_t add = l * 2u + (l < p.L ? 0u : kOob);
+        b.y[c] = __builtin_amdgcn_raw_buffer_load_b128(ry, off_y + add, 0, 0);
 #pragma unroll
-      for (int j = 0; j < FM; ++j) b.x[j][c] = __builtin_amdgcn_raw_buffer_load_b128(rx, off_x[j] + add, 0, 0);
-    }
-  };
-  f32x4 acc[FM];
+        for (int j = 0; j < FM; ++j) b.x[j][c] = __builtin_amdgcn_raw_buffer_load_b128(rx, off_x[j] + add, 0, 0);
+      }
+    };
+    f32x4 acc[FM];
 #pragma unroll
-  for (int j = 0; j < FM; ++j) acc[j] = f32x4{};
-  const bool tail = (p.L & 7) != 0;
-  // (what the last vector of l holds past the end may be anything)
-  auto clip = [&](u32x4 v, int l) {
-    bf16x8 b = __builtin_bit_cast(bf16x8, v);
-    if (tail) {
+    for (int j = 0; j < FM; ++j) acc[j] = f32x4{};
+    const bool tail = (p.L & 7) != 0;
+    // (what the last vector of l holds past the end may be anything)
+    auto clip = [&](u32x4 v, int l) {
+      bf16x8 b = __builtin_bit_cast(bf16x8, v);
+      if (tail) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = l + e < p.L ? b[e] : static_cast<__bf16>(0.0f);
-    }
-    return b;
-  };
-  auto use = [&](const Block& b, int kb) {
+        for (int e = 0; e < 8; ++e) b[e] = l + e < p.L ? b[e] : static_cast<__bf16>(0.0f);
+      }
+      return b;
+    };
+    auto use = [&](const Block& b, int kb) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int l = kb * 64 + 32 * c + 8 * g;
-      const bf16x8 vy = clip(b.y[c], l);
+      for (int c = 0; c < 2; ++c) {
+        const int l = kb * 64 + 32 * c + 8 * g;
+        const bf16x8 vy = clip(b.y[c], l);
 #pragma unroll
-      for (int j = 0; j < FM; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vy, clip(b.x[j][c], l), acc[j], 0, 0, 0);
-    }
-  };
-  if (wave < KB) {
-    constexpr int DEPTH = 4;
-    Block b[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      load(b[d], wave + d * WAVES);
-      __builtin_amdgcn_sched_barrier(0);   // (in the loop's order, which its waits count on)
-    }
-    for (int kb = wave; kb < KB; kb += DEPTH * WAVES) {
+        for (int j = 0; j < FM; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vy, clip(b.x[j][c], l), acc[j], 0, 0, 0);
+      }
+    };
+    if (wave < KB) {
+      constexpr int DEPTH = 4;
+      Block b[DEPTH];
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) {
-        use(b[d], kb + d * WAVES);
-        load(b[d], kb + (d + DEPTH) * WAVES);
-        __builtin_amdgcn_sched_barrier(0);
+        load(b[d], wave + d * WAVES);
+        __builtin_amdgcn_sched_barrier(0);   // (in the loop's order, which its waits count on)
+      }
+      for (int kb = wave; kb < KB; kb += DEPTH * WAVES) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          use(b[d], kb + d * WAVES);
+          load(b[d], kb + (d + DEPTH) * WAVES);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
-  }
-  if (wave > 0) {
+    if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) part[wave - 1][j][lane] = acc[j];
-  }
-  __syncthreads();
-  if (wave > 0) return;
+      for (int j = 0; j < FM; ++j) part[wave - 1][j][lane] = acc[j];
+    }
+    __syncthreads();
+    if (wave > 0) continue;
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
+    for (int j = 0; j < FM; ++j) {
 #pragma unroll
-    for (int w = 0; w < WAVES - 1; ++w) acc[j] = acc[j] + part[w][j][lane];
-    // the result block is C^T: the lane holds row r, columns 4 g .. + 3
-    const int i = i0 + 16 * j + r;
-    if (i < p.I) store4(p.z + static_cast<int64_t>(i) * a.ldz, j0 + 4 * g, a.J, acc[j]);
+      for (int q = 0; q < WAVES - 1; ++q) acc[j] = acc[j] + part[q][j][lane];
+      // the result block is C^T: the lane holds row r, columns 4 g .. + 3
+      const int i = i0 + 16 * j + r;
+      if (i < p.I) store4(p.z + static_cast<int64_t>(i) * a.ldz, j0 + 4 * g, a.J, acc[j]);
+    }
   }
 }
 
 int64_t most_row_tiles(const RArgs& r, int64_t bm) { return r.T / bm + std::min<int64_t>(r.experts, r.T); }
 
+// (a launch has fewer than 2^32 threads, of at most 256 each but for small grids)
+constexpr int64_t kMaxGrid = 0xffffff;
+
 // Workgroups for `groups` times `tiles_i` rows of tiles, eight per eight tiles.
 hipError_t grid_of(RArgs& r, int64_t groups, int64_t tiles_i, int bn, dim3& grid) {
   r.tiles_j = (r.J + bn - 1) / bn;
   const int64_t tiles = (tiles_i * r.tiles_j + 7) / 8 * 8;
-  if (tiles > 0x7ffffff0 || groups * tiles > 0x7ffffff0) return hipErrorInvalidValue;
+  if (tiles > kMaxGrid || groups * tiles > kMaxGrid) return hipErrorInvalidValue;
   grid = dim3(static_cast<unsigned>(groups * tiles));
   return hipSuccess;
 }
@@ -756,8 +774,9 @@ template <int FM>
 hipError_t launch_rows(RArgs& r, bool f32, hipStream_t s) {
   dim3 grid;
   if (const hipError_t e = grid_of(r, 1, most_row_tiles(r, 16 * FM), 16, grid); e != hipSuccess) return e;
-  if (f32) ragged_rows_kernel<FM, 4, float><<<grid, 256, 0, s>>>(r);
-  else ragged_rows_kernel<FM, 4, __bf16><<<grid, 256, 0, s>>>(r);
+  grid.x = std::min(grid.x, kRowGroups);
+  if (f32) ragged_rows_kernel<FM, kRowWaves, float><<<grid, 64 * kRowWaves, 0, s>>>(r);
+  else ragged_rows_kernel<FM, kRowWaves, __bf16><<<grid, 64 * kRowWaves, 0, s>>>(r);
   return hipGetLastError();
 }
 

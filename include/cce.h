@@ -495,9 +495,9 @@ cce_status cce_fused_allreduce_epilogue(cce_ctx* ctx, int n_ranks, cce_dtype par
  *
  * The conventions above hold (row-major matrices with ld a multiple of 8,
  * 16-byte aligned bases, asynchronous on `stream`, outputs that overlap
- * nothing, a zero extent is a no-op) with these additions.  ld of a product's
- * operand or result is at most 2^20 elements; operands and results may be
- * larger than 1 GiB.  Columns between a matrix's width and its ld are neither
+ * nothing, a zero extent is a no-op) with these additions.  Matrices have at
+ * most 2^30 rows; ld of a product's operand, result or scales is at most 2^20
+ * elements.  Operands and results may be larger than 1 GiB.  Columns between a matrix's width and its ld are neither
  * used nor written.  No call allocates.  Results do not depend on the stream
  * or on what else runs; the same call gives the same bits.
  *
@@ -523,7 +523,8 @@ cce_status cce_fused_allreduce_epilogue(cce_ctx* ctx, int n_ranks, cce_dtype par
  * x_t, CCE_F32 or CCE_BF16; weight [cols] of weight_t, CCE_F32 or CCE_BF16;
  * out of out_t: CCE_F32, CCE_BF16, or CCE_E4M3 with scales of 1 x 128 blocks
  * [rows, ceil(cols / 128)] (NULL otherwise).  The sum of squares, the norm
- * and the product with the weight are in fp32; out is rounded once.
+ * and the product with the weight are in fp32 or more; out is rounded once.  (A
+ * row whose sum of squares passes fp32's range, 3.4e38, has a norm of zero.)
  * eps must be a positive, normal fp32 number.  flags: must be 0.
  * ---------------------------------------------------------------------- */
 cce_status cce_rmsnorm(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_mat x_shape,

@@ -14,13 +14,14 @@ def up(v, step):
 
 
 class Padded:
-    """`t`: [rows, cols] with ld = cols rounded up to `step`, plus `pad`, and a row behind."""
+    """`t`: [rows, cols] with ld = cols rounded up to `step`, plus `pad`, and a row behind.  What
+    is not the matrix holds NaN of every type: it may neither be written nor reach a result."""
 
     def __init__(self, rows, cols, dtype, pad=0, step=8, value=None):
         self.rows, self.cols = rows, cols
         ld = up(cols, step) + up(pad, step)
         size = torch.empty((), dtype=dtype).element_size()
-        self.bytes = torch.full(((rows + 1) * ld * size,), 0x5a, dtype=torch.uint8, device=DEV)
+        self.bytes = torch.full(((rows + 1) * ld * size,), 0xff, dtype=torch.uint8, device=DEV)
         self.whole = self.bytes.view(dtype).view(rows + 1, ld)
         self.t = self.whole[:rows, :cols]
         if value is not None:
@@ -29,8 +30,8 @@ class Padded:
     def check_rest(self, what):
         size = self.t.element_size()
         b = self.bytes.view(self.rows + 1, -1)
-        assert bool((b[self.rows] == 0x5a).all()), f"{what}: the row behind was written"
-        assert bool((b[:, self.cols * size:] == 0x5a).all()), f"{what}: columns behind were written"
+        assert bool((b[self.rows] == 0xff).all()), f"{what}: the row behind was written"
+        assert bool((b[:, self.cols * size:] == 0xff).all()), f"{what}: columns behind were written"
 
 
 def f64(t):

@@ -323,6 +323,99 @@ def test_block_scaled_gemm_edges(ctx, m, ot):
     assert bool((z == 0).all())
 
 
+@pytest.mark.parametrize("m,n,k,ot", [
+    (40, 200, 16400, F32),        # few 64 x 64 tiles: waves along the contraction
+    (700, 500, 16016, F32),       # 64 x 64 tiles, scales in two panels
+    (2100, 2060, 31888, F32),     # 128 x 128 tiles, three panels
+    (1500, 1030, 16016, BF),      # 128 x 128 tiles of the 8-bit instruction
+    (4096, 4112, 16016, BF),      # 256 x 256 tiles
+    (4090, 4096, 272, BF),
+    (8, 4104, 16400, BF),
+])
+@pytest.mark.parametrize("scale_ld", [0, 3])
+def test_every_product_kernel_is_exact_on_small_integers(ctx, m, n, k, ot, scale_ld):
+    """Integers in [-2, 2] and scales of 1/2 to 2: sums of multiples of 1/4 below 2^22 are exact in
+    fp32 whatever the order, and in the fp64 product on the device; a contraction longer than the
+    124 blocks whose scales are held at a time, scale rows on words and off them."""
+    import collective_overlap_amd as cce
+    g = torch.Generator(device=DEV).manual_seed(m)
+    kb, nb = -(-k // 128), -(-n // 128)
+    a = torch.randint(-2, 3, (m, k), generator=g, device=DEV).float().to(E4)
+    b = torch.randint(-2, 3, (n, k), generator=g, device=DEV).float().to(E4)
+    def scales(rows):
+        s = torch.exp2(torch.randint(-1, 2, (rows, kb), generator=g, device=DEV).float())
+        t = torch.empty((rows, -(-kb // 4) * 4 + scale_ld), device=DEV, dtype=E8)[:, :kb]
+        t.copy_(s.to(E8))
+        return t
+    sa, sb = scales(m), scales(nb)
+    c = torch.empty((m, -(-n // 8) * 8), device=DEV, dtype=ot)[:, :n]
+    cce.cce_block_scaled_gemm(ctx, a, sa, b, sb, c)
+    wa = a.float().double() * sa.float().double().repeat_interleave(128, 1)[:, :k]
+    wb = b.float().double() * sb.float().double().repeat_interleave(128, 1)[:, :k].repeat_interleave(128, 0)[:n]
+    want = (wa @ wb.t().contiguous()).float().to(ot)
+    assert torch.equal(c, want), f"{int((c != want).sum())} of {want.numel()} differ"
+
+
+def test_more_rows_than_one_launch_takes(ctx):
+    """20 million rows of 8: more workgroups than a launch may have."""
+    import collective_overlap_amd as cce
+    rows = 20_000_003
+    x = torch.zeros((rows, 8), device=DEV, dtype=BF)
+    pick = torch.tensor([0, 1, (1 << 24) - 1, 1 << 24, rows - 2, rows - 1], device=DEV)
+    x[pick] = randn((len(pick), 8), 1, 1, BF).to(DEV)
+    w = torch.ones(8, device=DEV, dtype=BF)
+    out, q, s = torch.empty_like(x), torch.empty((rows, 8), device=DEV, dtype=E4), torch.empty((rows, 1), device=DEV, dtype=E8)
+    cce.cce_rmsnorm(ctx, x, w, out, EPS)
+    cce.cce_quantize_blocks(ctx, x, q, s, 1)
+    torch.cuda.synchronize()
+    X = f64(x[pick])
+    ref = ol.rmsnorm(X, np.ones(8), EPS)
+    within(f64(out[pick]), ref, (norm_tol(8) + HALF[BF]) * np.abs(ref) * 1.01, "out")
+    qr, sr = ol.quantize(X, 1)
+    np.testing.assert_array_equal(f64(q[pick]), qr)
+    np.testing.assert_array_equal(f64(s[pick]), sr)
+    assert int(torch.count_nonzero(out)) == int(torch.count_nonzero(x))
+
+
+def test_tensors_beyond_four_gibibytes(ctx):
+    """Rows past 2^32 bytes of the norm, its backward pass, the quantisation and the product."""
+    import collective_overlap_amd as cce
+    rows, cols, last = 1_100_000, 2048, 50
+    x = torch.zeros((rows, cols), device=DEV, dtype=BF)
+    x[-last:] = randn((last, cols), 1, 1, BF).to(DEV)
+    w = (1 + randn((cols,), 2, 0.2)).to(BF).to(DEV)
+    q, s = torch.empty((rows, cols), device=DEV, dtype=E4), torch.empty((rows, cols // 128), device=DEV, dtype=E8)
+    out, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(cols, device=DEV)
+    cce.cce_rmsnorm(ctx, x, w, out, EPS)
+    cce.cce_rmsnorm_backward(ctx, x, w, x, dx, dw, EPS)
+    cce.cce_quantize_blocks(ctx, x, q, s, 1)
+    b, sb = torch.empty((64, cols), device=DEV, dtype=E4), torch.empty((1, cols // 128), device=DEV, dtype=E8)
+    cce.cce_quantize_blocks(ctx, randn((64, cols), 3, 0.05).to(DEV), b, sb, 128)
+    torch.cuda.synchronize()
+    X, W = f64(x[-last:]), f64(w)
+    ref = ol.rmsnorm(X, W, EPS)
+    within(f64(out[-last:]), ref, (norm_tol(cols) + HALF[BF]) * np.abs(ref) * 1.01, "out")
+    rdx, rdw = ol.rmsnorm_backward(X, W, X, EPS)
+    n = X / np.sqrt(np.mean(X * X, axis=1, keepdims=True) + EPS)
+    within(f64(dw), rdw, (rows + norm_tol(cols) / U) * U * np.abs(X * n).sum(0), "dweight")
+    assert np.linalg.norm(f64(dx[-last:]) - rdx) <= 1e-2 * np.linalg.norm(rdx)
+    qr, sr = ol.quantize(X, 1)
+    np.testing.assert_array_equal(f64(q[-last:]), qr)
+    np.testing.assert_array_equal(f64(s[-last:]), sr)
+    del out, dx
+    qq = torch.zeros((2 * rows, cols), device=DEV, dtype=E4)
+    ss = torch.ones((2 * rows, cols // 128), device=DEV).to(E8)
+    assert qq.numel() > 1 << 32
+    qq[-last:], ss[-last:] = q[-last:], s[-last:]
+    for ot in (BF, F32):
+        c = torch.empty((2 * rows, 64), device=DEV, dtype=ot)
+        cce.cce_block_scaled_gemm(ctx, qq, ss, b, sb, c)
+        torch.cuda.synchronize()
+        ref, mag = ol.block_scaled_product(qr, sr, f64(b), f64(sb))
+        within(f64(c[-last:]), ref, (cols * U if ot == F32 else 2.0 ** -12) * mag + HALF[ot] * np.abs(ref), "c")
+        assert not bool(c[:-last].any())
+
+
 # ---- together -----------------------------------------------------------------------------
 def _layer(cce, ctx, t, stream=None):
     """Norm with the residual's addition and an 8-bit output, product with GELU, quantisation,

@@ -45,7 +45,7 @@ def build(case, pad):
     a = Padded(rows, k, BF, pad, value=randn((rows, k), 1, 1, BF))
     c = Padded(rows, n, BF, 0, value=randn((rows, n), 2, 1, BF))
     ld = -(-k // 8) * 8 + pad
-    w = torch.full((e, n + 1, ld), 9.0, dtype=BF, device=DEV)
+    w = torch.full((e, n + 1, ld), float("nan"), dtype=BF, device=DEV)
     b = w[:, :n, :k]
     b.copy_(randn((e, n, k), 3, 0.2, BF).to(DEV))
     return rows, n, k, off, a, b, c, torch.tensor(off, device=DEV)
@@ -180,3 +180,58 @@ def test_shared_weights_as_a_broadcast_input(ctx):
     cce.cce_ragged_gemm(ctx, a, w.repeat(2, 1, 1), o, y2)
     torch.cuda.synchronize()
     assert torch.equal(y1, y2)
+
+
+@pytest.mark.parametrize("rows,n,k,experts,top", [
+    (4096, 1024, 4096, 4, 3),      # 256 x 256 tiles, whole
+    (5000, 1100, 4104, 4, 3),      # 256 x 256 tiles, ragged
+    (3000, 700, 520, 2, 3),        # 128 x 128
+    (6000, 64, 72, 1, 2),          # 64 x 64, four groups, a long sum over the rows
+    (500, 1000, 8200, 5, 2),
+])
+def test_every_tile_size_is_exact_on_small_integers(ctx, rows, n, k, experts, top):
+    """Integers: every sum is below 2^24, so exact in fp32 and in the fp64 product on the device."""
+    import collective_overlap_amd as cce
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    def empty(*shape, dtype=F32):       # rows on multiples of 8
+        return torch.empty((*shape[:-1], -(-shape[-1] // 8) * 8), device=DEV, dtype=dtype)[..., :shape[-1]]
+    def ints(*shape):
+        return empty(*shape, dtype=BF).copy_(torch.randint(-top, top + 1, shape, generator=g, device=DEV))
+    a, b, c = ints(rows, k), ints(experts, n, k), ints(rows, n)
+    cut = sorted(torch.randint(0, rows - 5, (experts - 1,), generator=g, device=DEV).tolist())
+    off = [3] + [max(3, x) for x in cut] + [rows - 2]
+    o = torch.tensor(off, device=DEV)
+    y, da, db = empty(rows, n).fill_(5.0), empty(rows, k).fill_(5.0), empty(experts, n, k)
+    cce.cce_ragged_gemm(ctx, a, b, o, y)
+    cce.cce_ragged_gemm_dgrad(ctx, c, b, o, da)
+    cce.cce_ragged_gemm_wgrad(ctx, c, a, o, db)
+    ry, rda = torch.full((rows, n), 5.0, device=DEV), torch.full((rows, k), 5.0, device=DEV)
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        w = b[e].double()
+        ry[lo:hi] = (a[lo:hi].double() @ w.t().contiguous()).float()
+        rda[lo:hi] = (c[lo:hi].double() @ w).float()
+        assert torch.equal(db[e], (c[lo:hi].double().t().contiguous() @ a[lo:hi].double()).float()), f"db {e}"
+    assert torch.equal(y, ry) and torch.equal(da, rda)
+
+
+def test_rows_beyond_four_gibibytes(ctx):
+    """Operands of over 2^32 bytes: the last expert's rows are addressed past 32 bits."""
+    import collective_overlap_amd as cce
+    rows, n, k = 1_100_000, 64, 2048
+    a = torch.zeros((rows, k), device=DEV, dtype=BF)
+    assert a.numel() * 2 > 1 << 32
+    a[:100], a[-100:] = randn((100, k), 1, 1, BF).to(DEV), randn((100, k), 2, 1, BF).to(DEV)
+    b = randn((2, n, k), 3, 0.2, BF).to(DEV)
+    o = torch.tensor([0, 70, rows], device=DEV)
+    y, c = torch.empty((rows, n), device=DEV), torch.zeros((rows, n), device=DEV, dtype=BF)
+    c[-50:] = randn((50, n), 4, 1, BF).to(DEV)
+    da, db = torch.empty_like(a), torch.empty((2, n, k), device=DEV)
+    cce.cce_ragged_gemm(ctx, a, b, o, y)
+    cce.cce_ragged_gemm_dgrad(ctx, c, b, o, da)
+    cce.cce_ragged_gemm_wgrad(ctx, c, a, o, db)
+    torch.cuda.synchronize()
+    A, B, C = f64(a[-100:]), f64(b[1]), f64(c[-50:])
+    within(f64(y[-100:]), A @ B.T, k * U * (np.abs(A) @ np.abs(B).T), "c")
+    within(f64(da[-50:]), C @ B, n * U * (np.abs(C) @ np.abs(B)) + HALF[BF] * np.abs(C @ B), "da")
+    within(f64(db[1]), C.T @ A[-50:], 50 * U * (np.abs(C).T @ np.abs(A[-50:])), "db")
+    assert not bool(y[200:-200].any()) and not bool(da[200:-200].any()) and not bool(db[0].any())
