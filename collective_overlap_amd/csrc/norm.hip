@@ -189,12 +189,16 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NArgs a) {
   const __amdgpu_buffer_rsrc_t rw = row_rsrc<TW>(a.w, 0, 0, a.cols);
   Raw<TX> x[NV], r[NV];
   Raw<TW> w[NV];
+  // fp32 rows take two loads to a line, so the line is kept (1537 x 5005: 11.3
+  // us against 15.8 with nontemporal loads); bf16 rows take one (8192 x 12288:
+  // 118 us against 121 with plain loads).
+  constexpr bool kNT = sizeof(TX) == 2;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = load_raw<TX, true>(rx, t + i * TPR);
+  for (int i = 0; i < NV; ++i) x[i] = load_raw<TX, kNT>(rx, t + i * TPR);
   if (a.res) {
     const __amdgpu_buffer_rsrc_t rr = row_rsrc<TX>(a.res, row, a.ld_res, a.cols);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) r[i] = load_raw<TX, true>(rr, t + i * TPR);
+    for (int i = 0; i < NV; ++i) r[i] = load_raw<TX, kNT>(rr, t + i * TPR);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) w[i] = load_raw<TW, false>(rw, t + i * TPR);
