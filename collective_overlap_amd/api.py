@@ -100,7 +100,7 @@ def _on_device(ctx, ts):
 
 def _stream(stream, device) -> int:
     if stream is None:                           # the current one's handle, without a Stream object
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device if isinstance(device, int) else device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
