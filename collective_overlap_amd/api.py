@@ -524,7 +524,7 @@ def cce_rmsnorm(ctx: Context, x, weight, out, eps: float = 1e-5, residual=None, 
     _on_device(ctx, (x, weight, out, residual, residual_out, scales))
     check(lib().cce_rmsnorm(
         ctx.handle, _dtype(dtype), x.data_ptr(), cce_mat(rows, cols, ld), _ptr(residual), ld_r,
-        _ptr(residual_out), ld_ro, weight.data_ptr(), _dtype(weight.dtype), eps, out.data_ptr(),
+        _ptr(residual_out), ld_ro, weight.data_ptr(), _dtype(weight.dtype), float(eps), out.data_ptr(),
         CCE_E4M3 if quantized else _dtype(out.dtype), ld_o, _ptr(scales), ld_s, 0,
         _stream(stream, out.device)), "cce_rmsnorm")
     return out
@@ -554,7 +554,7 @@ def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: f
                          stream)
     check(lib().cce_rmsnorm_backward(
         ctx.handle, _dtype(dtype), x.data_ptr(), cce_mat(rows, cols, ld), weight.data_ptr(),
-        _dtype(weight.dtype), dout.data_ptr(), ld_d, _ptr(d_residual), ld_r, eps, dx.data_ptr(),
+        _dtype(weight.dtype), dout.data_ptr(), ld_d, _ptr(d_residual), ld_r, float(eps), dx.data_ptr(),
         ld_dx, _ptr(dweight), _ptr(ws), wsb, 0, _stream(stream, dx.device)),
         "cce_rmsnorm_backward")
     return dx
