@@ -183,9 +183,12 @@ def test_shared_weights_as_a_broadcast_input(ctx):
 
 
 @pytest.mark.parametrize("rows,n,k,experts,top", [
-    (4096, 1024, 4096, 4, 3),      # 256 x 256 tiles, whole
-    (5000, 1100, 4104, 4, 3),      # 256 x 256 tiles, ragged
-    (3000, 700, 520, 2, 3),        # 128 x 128
+    (6200, 2832, 2840, 8, 3),      # 256 x 256 tiles
+    (6200, 2833, 2843, 8, 3),      # 256 x 256 tiles, odd extents
+    (9000, 2816, 4096, 20, 3),     # 256 x 256 tiles, most experts part of a tile
+    (4096, 1024, 4096, 4, 3),      # 128 x 128 tiles, whole
+    (5000, 1100, 4104, 4, 3),      # 128 x 128 tiles, ragged
+    (3000, 700, 520, 2, 3),
     (6000, 64, 72, 1, 2),          # 64 x 64, four groups, a long sum over the rows
     (500, 1000, 8200, 5, 2),
 ])
@@ -212,6 +215,27 @@ def test_every_tile_size_is_exact_on_small_integers(ctx, rows, n, k, experts, to
         rda[lo:hi] = (c[lo:hi].double() @ w).float()
         assert torch.equal(db[e], (c[lo:hi].double().t().contiguous() @ a[lo:hi].double()).float()), f"db {e}"
     assert torch.equal(y, ry) and torch.equal(da, rda)
+
+
+@pytest.mark.parametrize("counts", [[256] * 22, [256] * 32 + [0], [1] * 3 + [5800], [256] * 33, [300] * 17, [257] * 19,
+                                    [2048, 100, 2048, 1500]])
+def test_large_tiles_of_many_counts(ctx, counts):
+    """Counts of tiles (12 to a row of them) on both sides of a round of the compute units, one
+    round, two; experts of exactly a tile's rows, of one more, of one."""
+    import collective_overlap_amd as cce
+    rows, n, k, e = sum(counts), 3000, 136, len(counts)
+    g = torch.Generator(device=DEV).manual_seed(e)
+    a = torch.randint(-3, 4, (rows, k), generator=g, device=DEV).to(BF)
+    b = torch.randint(-3, 4, (e, n, k), generator=g, device=DEV).to(BF)
+    c = torch.randint(-3, 4, (rows, k), generator=g, device=DEV).to(BF)
+    off = torch.tensor([0] + counts, device=DEV).cumsum(0)
+    y, da = torch.full((rows, n), 5.0, device=DEV), torch.full((rows, n), 5.0, device=DEV)
+    cce.cce_ragged_gemm(ctx, a, b, off, y)
+    bt = b.transpose(1, 2).contiguous()                    # [e, k, n]: the gradient has n columns
+    cce.cce_ragged_gemm_dgrad(ctx, c, bt, off, da)
+    for i, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        assert torch.equal(y[lo:hi], (a[lo:hi].double() @ bt[i].double()).float()), f"expert {i}"
+        assert torch.equal(da[lo:hi], (c[lo:hi].double() @ bt[i].double()).float()), f"gradient, expert {i}"
 
 
 def test_rows_beyond_four_gibibytes(ctx):
