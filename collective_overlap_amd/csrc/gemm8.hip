@@ -10,7 +10,8 @@
 //                      matrix cores, because the 8-bit instruction's own sums
 //                      of 64 products keep about 16 bits (measured: 1.5e-5
 //                      of the result's norm against 1e-7).
-//   gemm8_rows_kernel  few rows: bound by reading B once; widened too.
+//   gemm8_rows_kernel  few rows, and small products: bound by reading B once, or
+//                      by one trip to memory; widened too.
 
 #include <hip/hip_runtime.h>
 
@@ -624,14 +625,23 @@ cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
   if (tiles(64) > 0xffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
   const bool f32 = L.out_t == CCE_F32;
   // Few rows, or so few 64 x 64 tiles that a tile's length in K is the time
-  // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 13 against 15).  Two
-  // waves per workgroup where the columns alone fill the GPU (4 x 12288 x
-  // 6144: 15.4 us against 16.2 with four).
+  // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 13 against 15).  Up to
+  // 8 rows in 16 columns per workgroup, of two waves where the columns alone
+  // fill the GPU (4 x 12288 x 6144: 15.5 us against 16.2 with four); more rows,
+  // which A's own reading begins to cost, in 32 columns, or in 64 where there
+  // are enough (16 x 12288 x 6144: 21.1 us in 16, 20.8 in 32, 17.2 in 64; 16 x
+  // 5000 x 4096: 11.9, 9.3, 12.8; 16 x 4096 x 4096: 7.3, 9.2; 32 x 12288 x 6144:
+  // 21.6 in 64, 24.5 in 64 x 64 tiles; 32 x 4096 x 4096: 12.7 in 32, 16.5).
   // Then the largest tiles that come close to one per compute unit; with fewer
   // than 96 of the 128 x 128 ones the deeper 64 x 64 ones are faster (1000 x
   // 1000 x 4096: 18 us against 22; 128 x 12288 x 4096, 96 tiles: 23 against 22).
-  if (L.M <= 16 || tiles(64) <= 32) {
-    if (L.N > 4096) launch_rows<1, 1, 2>(a, f32, s);
+  if (L.M <= 32 || tiles(64) <= 32) {
+    const bool more = L.M > 8 && L.M <= 32;
+    if (more && L.N > 8192 && L.M <= 16) launch_rows<1, 4, 2>(a, f32, s);
+    else if (more && L.N > 8192) launch_rows<2, 4, 2>(a, f32, s);
+    else if (more && L.N > 4096 && L.M <= 16) launch_rows<1, 2, 4>(a, f32, s);
+    else if (more && L.N > 2048 && L.M > 16) launch_rows<2, 2, 4>(a, f32, s);
+    else if (L.N > 4096) launch_rows<1, 1, 2>(a, f32, s);
     else launch_rows<1, 1, 4>(a, f32, s);
   } else if (!f32 && tiles(256) >= 256) {
     launch_tiles<256, 256>(a, s);

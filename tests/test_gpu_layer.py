@@ -247,7 +247,8 @@ def operands(m, n, k, seed, pad=0):
 
 PRODUCTS = [(1, 1, 16), (1, 64, 128), (1, 1000, 4096), (2, 130, 272), (4, 4096, 1040), (8, 520, 2048), (16, 256, 512),
             (17, 129, 144), (32, 1000, 528), (33, 200, 640), (64, 640, 256), (65, 72, 4224), (128, 128, 128),
-            (129, 300, 384), (255, 257, 400), (333, 1000, 2064), (512, 384, 1024), (1030, 520, 272)]
+            (129, 300, 384), (255, 257, 400), (333, 1000, 2064), (512, 384, 1024), (1030, 520, 272), (12, 4100, 400), (20, 2600, 1040), (9, 8200, 272),
+            (25, 8210, 1040), (32, 2049, 144)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
