@@ -14,6 +14,18 @@ import pytest
 from collective_overlap_amd import build
 
 
+@pytest.fixture(scope="module")
+def asm(tmp_path_factory):
+    """The device assembly of a source, compiled once."""
+    done = {}
+
+    def get(name):
+        if name not in done:
+            done[name] = _asm(tmp_path_factory.mktemp("asm"), name)
+        return done[name]
+    return get
+
+
 def _asm(tmp, name):
     hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
     if not os.path.exists(hipcc):
@@ -41,8 +53,8 @@ def _loop_blocks(body, mfmas):
 @pytest.mark.parametrize("source,kernel,tile,mfmas", [
     ("ragged", "ragged_kernel", "Li256ELi256E", 64), ("ragged", "ragged_kernel", "Li128ELi128E", 16),
     ("gemm8", "gemm8_kernel", "Li256ELi256E", 32), ("gemm8", "gemm8_kernel", "Li128ELi128E", 8)])
-def test_one_full_wait_per_tile(tmp_path, source, kernel, tile, mfmas):
-    text = _asm(tmp_path, source)
+def test_one_full_wait_per_tile(asm, source, kernel, tile, mfmas):
+    text = asm(source)
     names = [n for n in re.findall(r"^(_ZN3cce12_GLOBAL__N_1\S+):", text, re.M) if kernel + "I" + tile in n]
     assert len(names) >= 2
     for name in names:
