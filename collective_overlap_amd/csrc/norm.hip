@@ -59,8 +59,13 @@ __device__ __forceinline__ double row_sum(float v, double* sh) {
   return s;
 }
 
+// 1 / sqrt(mean + eps), from the fp32 instruction's value and one step of
+// Newton's method in fp64 (relative error 1.5 times the square of the first
+// one's 1e-7); a mean past fp32's range gives 0.
 __device__ __forceinline__ float rstd_of(double squares, int cols, float eps) {
-  return static_cast<float>(1.0 / sqrt(squares / cols + eps));
+  const double x = squares * (1.0 / cols) + eps;
+  const double r = __builtin_amdgcn_rsqf(static_cast<float>(x));
+  return r > 0.0 ? static_cast<float>(r * (1.5 - 0.5 * x * r * r)) : static_cast<float>(r);
 }
 
 __device__ __forceinline__ void load_weight(const NArgs& a, int j, float (&w)[8]) {
@@ -228,6 +233,54 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NArgs a) {
   }
 }
 
+// Narrow rows (per-head norms): TPR threads to a row, one vector each, so that
+// a wave takes 64 / TPR rows, and kRowsOfThread rows of a thread in flight
+// together (400000 x 128 bf16: 37 us, 5.5 TB/s; a wave per row took 109).
+constexpr int kRowsOfThread = 2;
+
+// Sum over groups of TPR lanes, in fp64.
+template <int TPR>
+__device__ __forceinline__ double lane_sum(float v) {
+  double s = v;
+#pragma unroll
+  for (int m = TPR / 2; m >= 1; m >>= 1) s += __shfl_xor(s, m);
+  return s;
+}
+
+template <typename TX, typename TW, typename TO, int TPR>
+__global__ __launch_bounds__(kThreads) void rmsnorm_narrow_kernel(NArgs a) {
+  constexpr int RPW = kThreads / TPR, U = kRowsOfThread;
+  const int t = threadIdx.x % TPR, j = 8 * t;
+  const int64_t row0 = a.row0 + static_cast<int64_t>(blockIdx.x) * (RPW * U) + threadIdx.x / TPR;
+  float v[U][8], r[U][8], w[8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + u * RPW;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = r[u][e] = 0.0f;
+    if (row < a.rows) {
+      load8<TX, true>(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, v[u]);
+      if (a.res) load8<TX, true>(reinterpret_cast<const TX*>(a.res) + row * a.ld_res, j, a.cols, r[u]);
+    }
+  }
+  load8(reinterpret_cast<const TW*>(a.w), j, a.cols, w);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + u * RPW;
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (a.res) v[u][e] = rounded<TX>(v[u][e] + r[u][e]);
+      ss += v[u][e] * v[u][e];
+    }
+    const float rstd = rstd_of(lane_sum<TPR>(ss), a.cols, a.eps);
+    if (row < a.rows) {     // (the same for the 16 lanes of a scale)
+      if (a.res_out && j < a.cols) store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, j, a.cols, v[u]);
+      finish<TO>(a, row, t, v[u], w, rstd);
+    }
+  }
+}
+
 // Rows too wide for the registers: one workgroup per row, two passes over it
 // (the second mostly from the caches).
 template <typename TX, typename TO>
@@ -337,7 +390,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
       __builtin_amdgcn_sched_barrier(0);   // (one vector widened at a time)
     }
     const float rstd = rstd_of(row_sum<TPR / 64>(ss, sh), a.cols, a.eps);
-    const float mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2) / a.cols) * rstd;   // of w dy n
+    const float mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;   // of w dy n
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = 8 * (t + i * TPR);
@@ -372,6 +425,63 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
   }
 }
 
+// Narrow rows: as rmsnorm_narrow_kernel; the workgroup's rows join their sums of
+// dw through LDS, in order, to one line (400000 x 128 bf16: 60 us, 5.1 TB/s; a
+// wave per row took 252).
+template <typename TX, typename TW, int TPR>
+__global__ __launch_bounds__(kThreads) void rmsnorm_backward_narrow_kernel(BArgs a) {
+  constexpr int RPW = kThreads / TPR;
+  __shared__ float sh[RPW][8 * TPR + 4];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, j = 8 * t;
+  struct Row {
+    float x[8], d[8], r[8];
+  };
+  auto load = [&](Row& q, int64_t row) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q.x[e] = q.d[e] = q.r[e] = 0.0f;
+    if (row < a.rows) {
+      load8<TX, true>(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, q.x);
+      load8<TX, true>(reinterpret_cast<const TX*>(a.dout) + row * a.ld_dout, j, a.cols, q.d);
+      if (a.dres) load8<TX, true>(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, j, a.cols, q.r);
+    }
+  };
+  float w[8], dw[8] = {};
+  load8(reinterpret_cast<const TW*>(a.w), j, a.cols, w);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * RPW;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + sub;
+  Row next;
+  load(next, row);
+  for (; row - sub < a.rows; row += step) {      // (the same for the workgroup)
+    const Row q = next;
+    load(next, row + step);
+    float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ss += q.x[e] * q.x[e];
+      dot += q.d[e] * w[e] * q.x[e];
+    }
+    const float rstd = rstd_of(lane_sum<TPR>(ss), a.cols, a.eps);
+    const float mean = static_cast<float>(lane_sum<TPR>(dot) * (1.0 / a.cols)) * rstd;   // of w dy n
+    float g[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float n = q.x[e] * rstd;
+      dw[e] += q.d[e] * n;
+      g[e] = (q.d[e] * w[e] - n * mean) * rstd + q.r[e];
+    }
+    if (row < a.rows && j < a.cols) store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, j, a.cols, g);
+  }
+  if (!a.dw) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sh[sub][j + e] = dw[e];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= a.cols || c >= 8 * TPR) return;
+  float s = sh[0][c];
+  for (int i = 1; i < RPW; ++i) s += sh[i][c];
+  a.part[static_cast<int64_t>(blockIdx.x) * a.ld_part + c] = s;
+}
+
 // Rows too wide for the registers: dx by two passes over each row, which also
 // leave 1 / root in the workspace, and dw by a pass of its own (below).
 template <typename TX>
@@ -399,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
       }
     }
     const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
-    const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) / a.cols) * rstd;
+    const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;
     if (tid == 0) a.rstd[row] = rstd;
     for (int i = tid; i < vectors; i += kThreads) {
       float v[8], d[8], w[8], g[8];
@@ -584,9 +694,16 @@ constexpr int64_t kMaxForwardCols = 16384, kMaxBackwardCols = 12288;
 // room for no more (8192 x 12288: 149 us against 156 with two).  Wider: chunks
 // of rows, enough for the GPU and few enough that the lines stay a small part
 // of the traffic.
-int64_t backward_groups(int64_t cols) { return cols > 4096 ? 256 : 512; }
+// Narrow: a line per workgroup of 16 or 8 rows, four per compute unit.
+constexpr int64_t kMaxNarrowCols = 256;
+int narrow_rows_per_group(int64_t cols) { return cols <= 128 ? 16 : 8; }
+int64_t backward_groups(int64_t cols) { return cols > 4096 ? 256 : cols > kMaxNarrowCols ? 512 : 1024; }
 int backward_rows_per_group(int64_t cols) { return cols <= 1024 ? 4 : 1; }
 int dweight_lines(int64_t rows, int64_t cols) {
+  if (cols <= kMaxNarrowCols) {
+    const int rpw = narrow_rows_per_group(cols);
+    return static_cast<int>(std::min(backward_groups(cols), (rows + rpw - 1) / rpw));
+  }
   if (cols <= kMaxBackwardCols) {
     const int rpw = backward_rows_per_group(cols);
     return static_cast<int>(std::min(backward_groups(cols), (rows + rpw - 1) / rpw) * rpw);
@@ -603,6 +720,13 @@ void launch_norm(NArgs a, hipStream_t s) {
     for (a.row0 = 0; a.row0 < a.rows; a.row0 += kMaxGrid * RPW)
       rmsnorm_kernel<TX, TW, TO, RPW, NV><<<grid_for((a.rows - a.row0 + RPW - 1) / RPW), kThreads, 0, s>>>(a);
   };
+  auto narrow = [&](auto tpr) {
+    constexpr int64_t TPR = decltype(tpr)::value, each = kThreads / TPR * kRowsOfThread;
+    for (a.row0 = 0; a.row0 < a.rows; a.row0 += kMaxGrid * each)
+      rmsnorm_narrow_kernel<TX, TW, TO, TPR><<<grid_for((a.rows - a.row0 + each - 1) / each), kThreads, 0, s>>>(a);
+  };
+  if (a.cols <= 128) return narrow(std::integral_constant<int, 16>{});
+  if (a.cols <= kMaxNarrowCols) return narrow(std::integral_constant<int, 32>{});
   // A wave per row up to 1024 columns, a workgroup of four per row above.
   if (a.cols <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
   else if (a.cols <= 1024) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
@@ -628,6 +752,13 @@ void launch_backward(const BArgs& a, hipStream_t s) {
     const int64_t groups = std::min<int64_t>(backward_groups(a.cols), (a.rows + RPW - 1) / RPW);
     rmsnorm_backward_kernel<TX, TW, T, RPW, NV><<<dim3(static_cast<unsigned>(groups)), T, 0, s>>>(a);
   };
+  auto narrow = [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    rmsnorm_backward_narrow_kernel<TX, TW, TPR>
+        <<<dim3(static_cast<unsigned>(dweight_lines(a.rows, a.cols))), kThreads, 0, s>>>(a);
+  };
+  if (a.cols <= 128) return narrow(std::integral_constant<int, 16>{});
+  if (a.cols <= kMaxNarrowCols) return narrow(std::integral_constant<int, 32>{});
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I3 = std::integral_constant<int, 3>;

@@ -37,7 +37,7 @@ def norm_tol(cols):
 
 
 SHAPES = [(1, 8), (3, 1), (5, 7), (2, 64), (4, 127), (4, 128), (3, 129), (7, 1000), (2, 2048), (3, 4096),
-          (2, 5005), (3, 8192), (5, 12288), (2, 16384), (2, 16392), (2, 40001), (300, 520)]
+          (2, 5005), (3, 8192), (5, 12288), (2, 16384), (2, 16392), (2, 40001), (300, 520), (4100, 96), (1501, 250), (33, 256)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -358,11 +358,11 @@ def test_every_product_kernel_is_exact_on_small_integers(ctx, m, n, k, ot, scale
 
 
 def test_more_rows_than_one_launch_takes(ctx):
-    """20 million rows of 8: more workgroups than a launch may have."""
+    """134 million rows of 8: more workgroups than a launch may have."""
     import collective_overlap_amd as cce
-    rows = 20_000_003
+    rows = (1 << 27) + 70_003
     x = torch.zeros((rows, 8), device=DEV, dtype=BF)
-    pick = torch.tensor([0, 1, (1 << 24) - 1, 1 << 24, rows - 2, rows - 1], device=DEV)
+    pick = torch.tensor([0, 1, (1 << 24) - 1, 1 << 24, (1 << 27) - 1, 1 << 27, rows - 2, rows - 1], device=DEV)
     x[pick] = randn((len(pick), 8), 1, 1, BF).to(DEV)
     w = torch.ones(8, device=DEV, dtype=BF)
     out, q, s = torch.empty_like(x), torch.empty((rows, 8), device=DEV, dtype=E4), torch.empty((rows, 1), device=DEV, dtype=E8)
@@ -376,6 +376,16 @@ def test_more_rows_than_one_launch_takes(ctx):
     np.testing.assert_array_equal(f64(q[pick]), qr)
     np.testing.assert_array_equal(f64(s[pick]), sr)
     assert int(torch.count_nonzero(out)) == int(torch.count_nonzero(x))
+    del out
+    dx, dw = torch.empty_like(x), torch.empty(8, device=DEV)
+    cce.cce_rmsnorm_backward(ctx, x, w, x, dx, dw, EPS)
+    torch.cuda.synchronize()
+    rdx, rdw = ol.rmsnorm_backward(X, np.ones(8), X, EPS)
+    n = X / np.sqrt(np.mean(X * X, axis=1, keepdims=True) + EPS)
+    mag = (np.abs(X) + np.abs(n) * np.mean(np.abs(X * n), axis=1, keepdims=True)) * np.abs(n / X)
+    within(f64(dx[pick]), rdx, (chain(8) + 3 * norm_tol(8) / U + 8) * U * mag + HALF[BF] * np.abs(rdx), "dx")
+    # (adding a row of zeros is exact: the sums are those of the picked rows)
+    within(f64(dw), rdw, (len(pick) + norm_tol(8) / U + 4) * U * np.abs(X * n).sum(0), "dweight")
 
 
 def test_tensors_beyond_four_gibibytes(ctx):
