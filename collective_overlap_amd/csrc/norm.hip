@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_wide_kernel(NArgs a) {
     for (int i = tid; i < vectors; i += kThreads) {
       float v[8];
       load_sum<TX>(a, row, 8 * i, v);
-  #pragma unroll
+#pragma unroll
       for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
       if (a.res_out) store8(reinterpret_cast<TX*>(a.res_out) + row * a.ld_res_out, 8 * i, a.cols, v);
     }
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
       load8(x, 8 * i, a.cols, v);
       load8(dy, 8 * i, a.cols, d);
       load_weight(wa, 8 * i, w);
-  #pragma unroll
+#pragma unroll
       for (int e = 0; e < 8; ++e) {
         ss += v[e] * v[e];
         dot += d[e] * w[e] * v[e];
@@ -516,12 +516,12 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
       load8(x, 8 * i, a.cols, v);
       load8(dy, 8 * i, a.cols, d);
       load_weight(wa, 8 * i, w);
-  #pragma unroll
+#pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = (d[e] * w[e] - v[e] * rstd * mean) * rstd;
       if (a.dres) {
         float r[8];
         load8(reinterpret_cast<const TX*>(a.dres) + row * a.ld_dres, 8 * i, a.cols, r);
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < 8; ++e) g[e] += r[e];
       }
       store8(reinterpret_cast<TX*>(a.dx) + row * a.ld_dx, 8 * i, a.cols, g);
