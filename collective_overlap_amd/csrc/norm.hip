@@ -327,7 +327,7 @@ struct BArgs {
 // two sums and its dx, and a thread keeps the sums of its columns of dw over
 // the rows its workgroup takes (every gridDim.x-th group of RPW); they go to
 // the workspace at the end, a line per group of threads, and column_sum_kernel
-// adds the lines in their order.  Bound by HBM: 8192 x 12288 bf16 149 us, 5.4
+// adds the lines in their order.  Bound by HBM: 8192 x 12288 bf16 146 us, 5.5
 // TB/s (two passes and a third for dw: 267; without the loads ahead: 171).
 template <typename TX, typename TW, int THREADS, int RPW, int NV>
 __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
