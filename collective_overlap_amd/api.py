@@ -229,18 +229,20 @@ def _workspace(need, device, workspace, stream=None):
     """The caller's workspace (the library checks its size), or a temporary
     one of need() bytes.  A temporary one is freed when the call returns,
     while the work that uses it may still be queued on `stream` (the copy
-    stream joins back into it).  When that is not the current stream, the
-    caching allocator is told, so that it does not hand the memory out again
-    before `stream` has finished with it."""
+    stream joins back into it).  It comes from that stream's own pool of the
+    caching allocator, whose blocks only later work on the same stream can
+    get: a block of the current stream's pool may still be in use there."""
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
     nbytes = need()
     if nbytes == 0:
         return None, 0
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     s = _torch_stream(stream, device)
-    if s != torch.cuda.current_stream(device):
-        workspace.record_stream(s)
+    if s == torch.cuda.current_stream(device):
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(s):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, nbytes
 
 

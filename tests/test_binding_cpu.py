@@ -68,3 +68,35 @@ def test_host_tensors_are_rejected_before_the_library_sees_them():
         cce.cce_looped_einsum_reducescatter_epilogue(_Ctx(), "slice_lhs_rows", [_t((32, 64))] * 2,
                                                      [_t((24, 64))] * 2, None, None,
                                                      [_t((16, 24))] * 2, 0.1)
+
+
+@pytest.mark.parametrize("given", [None, "side"])
+def test_a_temporary_workspace_comes_from_the_pool_of_its_stream(monkeypatch, given):
+    """A block of the current stream's pool may still be in use there when another stream gets
+    it: the memory is asked for while the stream that will use it is the current one."""
+    from collective_overlap_amd import api
+    current, asked = ["main"], []
+
+    class use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current.append(self.s)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    empty = torch.empty
+
+    def recorded(*a, **k):
+        asked.append(current[-1])
+        return empty(*a, **k)
+
+    monkeypatch.setattr(api, "_torch_stream", lambda s, d: "main" if s is None else s)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[-1])
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    ws, n = api._workspace(lambda: 64, torch.device("cpu"), None, given)
+    assert (n, ws.numel()) == (64, 64) and asked == [given or "main"] and current == ["main"]
