@@ -308,13 +308,14 @@ constexpr int kDevCoherent = 16;   // buffer instruction cache policy: sc1
 template <bool WHOLE = false>
 __device__ __forceinline__ void store_dev4(__amdgpu_buffer_rsrc_t r, uint32_t off, f32x4 v, int n,
                                            int N) {
+  // (the whole vector at once: this compiler's bit cast of one element of a
+  // vector reads element 0, whichever is named)
+  const u32x4 w = __builtin_bit_cast(u32x4, v);
   if (WHOLE || n + 3 < N) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, kDevCoherent);
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, kDevCoherent);
   } else {
     for (int e = 0; e < 4; ++e)
-      if (n + e < N)
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[e]), r, off + 4 * e, 0,
-                                              kDevCoherent);
+      if (n + e < N) __builtin_amdgcn_raw_buffer_store_b32(w[e], r, off + 4 * e, 0, kDevCoherent);
   }
 }
 

@@ -209,3 +209,48 @@ def test_fine_noalloc_equals_workspace_call(ctx):
     ctx.check_signals()
     for r in range(n):
         assert torch.equal(_ints(x[r]), _ints(y[r])), f"rank {r}"
+
+
+def _padded(rows, cols, dtype, value=None):
+    """[rows, cols] inside rows of a multiple of 8."""
+    t = torch.full((rows, -(-cols // 8) * 8), float("nan"), device=DEV, dtype=dtype)[:, :cols]
+    return t if value is None else t.copy_(value)
+
+
+@pytest.mark.parametrize("cols", [34, 35, 263, 518])
+@pytest.mark.parametrize("form", EPI_FORMS)
+@pytest.mark.parametrize("in_dt", [torch.bfloat16, torch.float32])
+def test_epilogue_fine_equals_event_form_on_widths_of_no_multiple_of_four(ctx, cols, form, in_dt):
+    """Two or three columns in the last quad of a row: each is published with its own value."""
+    import collective_overlap_amd as cce
+    mode, n, s, k = "slice_lhs_rows", 4, 72, 128
+    print(f"[gpu] fine-grained epilogue {form} {cols} columns {in_dt}", flush=True)
+    a, b, oshape = _inputs(mode, n, (s, k, cols), seed=cols, in_dt=in_dt)
+    bias = W.normal((cols,), 0.02, 90, device=DEV, dtype=torch.float32)
+    res = [_padded(s, cols, torch.float32, W.normal(oshape, 1.0, 100 + r, device=DEV, dtype=torch.float32)) for r in range(n)]
+    outs = {}
+    for fine in (0, cce.CCE_FLAG_FINE_GRAINED):
+        o = [_padded(s, cols, torch.float32) for _ in range(n)]
+        cce.cce_looped_einsum_reducescatter_epilogue(ctx, mode, a, b, bias, res, o, 0.1, 5, 2,
+                                                     mask_row0=[r * s for r in range(n)], mask_col0=0,
+                                                     mask_ld=cols, flags=_flags(cce, form) | fine)
+        outs[fine] = [t.contiguous() for t in o]
+    ctx.check_signals()
+    for r in range(n):
+        assert torch.equal(_ints(outs[0][r]), _ints(outs[cce.CCE_FLAG_FINE_GRAINED][r])), \
+            f"rank {r}: fine-grained and event forms differ"
+
+
+@pytest.mark.parametrize("cols", [34, 263])
+@pytest.mark.parametrize("in_dt", [torch.bfloat16, torch.float32])
+def test_fine_align_and_sum_of_widths_of_no_multiple_of_four_against_oracle(ctx, cols, in_dt):
+    import collective_overlap_amd as cce
+    mode, n, s, k = "slice_lhs_rows", 4, 40, 64
+    a, b, oshape = _inputs(mode, n, (s, k, cols), seed=7 * cols, in_dt=in_dt)
+    out = [_padded(s, cols, torch.float32) for _ in range(n)]
+    cce.cce_looped_einsum_reducescatter(ctx, mode, a, b, out,
+                                        flags=cce.CCE_FLAG_FUSED_PERMUTE | cce.CCE_FLAG_BIDIRECTIONAL | cce.CCE_FLAG_FINE_GRAINED)
+    ctx.check_signals()
+    ref = oe.einsum_reducescatter(mode, [np64(x) for x in a], [np64(x).T for x in b])
+    for r in range(n):
+        assert_f32_close(np64(out[r]), ref[r], f"rank {r}")
