@@ -68,10 +68,9 @@ __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 // load to LDS in flight and waits for them.)
 __device__ __forceinline__ int read_byte(const __attribute__((address_space(3))) uint8_t* __restrict__ p) { return *p; }
 
-// 8 e4m3 values times their block's scale, as bf16.  The instruction takes
-// the scale as a float's exponent, which is E8M0's own encoding.  Exact: a
-// e4m3 value has 4 significant bits and bf16 float's exponents (results below
-// 2^-126 are rounded to bf16's subnormals).
+// 8 e4m3 values times a power of two (a float's exponent, which is E8M0's own
+// encoding; 255 gives NaN), as bf16.  Exact where the products are normal bf16
+// numbers: a e4m3 value has 4 significant bits.
 __device__ __forceinline__ bf16x8 scaled(u32x2 v, float scale) {
   bf16x8 r;
 #pragma unroll
@@ -86,7 +85,32 @@ __device__ __forceinline__ bf16x8 scaled(u32x2 v, float scale) {
   return r;
 }
 
-__device__ __forceinline__ float scale_float(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+// The factors of a block of A's rows (FM of the lane's) and of a block of B,
+// for `scaled`.  The two scales act as one, 2^e with e = sa + sb - 254, which
+// goes to A, so that a scale that bf16 cannot hold does no harm where the other
+// one brings the product back.  448 2^e fits bf16 up to e = 119.  Where one of
+// the wave's rows has more, B takes 2^9: what A's values then overflow bf16
+// with is past fp32 with the least of B's, 2^-9, too; and from e = 137 on, where
+// A's factor would pass 2^127, 2^18 (A's least value is 2^-9 as well).
+// The products are exact from e = -117 on, where A's values are normal (-108 or
+// -99 beside such a row); below they lose bits to bf16's subnormals, and A's
+// factor is 2^-127 at least.  A scale of 255 stands for NaN.
+template <int FM>
+__device__ __forceinline__ void block_factors(const int (&sa)[FM], int sb, float (&fa)[FM], float& fb) {
+  bool nan[FM];
+  int top = 0;
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    nan[j] = max(sa[j], sb) == 255;
+    top = max(top, nan[j] ? 0 : sa[j] + sb);
+  }
+  int over = 0;
+  if (__any(top > 254 + 119)) over = __any(top > 254 + 136) ? 18 : 9;
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+    fa[j] = __builtin_bit_cast(float, (nan[j] ? 255 : min(max(sa[j] + sb - 127 - over, 0), 254)) << 23);
+  fb = __builtin_bit_cast(float, (127 + over) << 23);
+}
 
 // Tile of a workgroup: each of the 8 XCDs (dealt workgroups in turn) gets a
 // contiguous range of tiles, walked in bands of 4 tile rows, so that the
@@ -389,6 +413,13 @@ __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
 #pragma unroll
     for (int d = 0; d < NS - 1; ++d) load(d, d * kBK);
   }
+  int sa[FM], sb;
+  auto read_scales = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) sa[j] = read_byte((lds_bytes)(panel + pa0 + 32 * j * kPanel + k));
+    sb = read_byte((lds_bytes)(panel + pb0 + k));
+  };
+  float fa[FM], fb;             // of tile kt
   int cur = 0, kp = 0;          // buffer of tile kt, its block in the panel
   for (int kt = 0; kt < KT; ++kt) {
     wait_vmcnt<(NS - 2) * N_DMA>();
@@ -400,9 +431,11 @@ __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
     __syncthreads();
     const int prv = cur == 0 ? NS - 1 : cur - 1;
     load(prv, (kt + NS - 1) * kBK);
-    float fa[FM], fb = scale_float(read_byte((lds_bytes)(panel + pb0 + kp)));
-#pragma unroll
-    for (int j = 0; j < FM; ++j) fa[j] = scale_float(read_byte((lds_bytes)(panel + pa0 + 32 * j * kPanel + kp)));
+    if (kp == 0) {              // (the others' factors were formed in the tile before)
+      read_scales(0);
+      block_factors(sa, sb, fa, fb);
+    }
+    read_scales(min(kp + 1, kPanel - 1));
     const char* s = smem + cur * STAGE;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -425,6 +458,7 @@ __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
         }
       }
     }
+    block_factors(sa, sb, fa, fb);
     ++kp;
     cur = cur + 1 == NS ? 0 : cur + 1;
   }
@@ -500,7 +534,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
   for (int i = 0; i < FN; ++i) off_b[i] = n0 + 16 * i + r < a.N ? static_cast<uint32_t>(16 * i + r) * a.ldb : kOob;
   struct Block {
     u32x4 b[FN][2], a[FM][2];
-    uint32_t sb, sa[FM];
+    int sb, sa[FM];
   };
   auto load = [&](Block& x, int kb) {
 #pragma unroll
@@ -525,7 +559,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
 #pragma unroll
     for (int i = 0; i < FN; ++i) acc[j][i] = f32x4{};
   auto use = [&](const Block& x) {
-    const float fb = scale_float(x.sb);
+    float fa[FM], fb;
+    block_factors(x.sa, x.sb, fa, fb);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -535,7 +570,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
         for (int i = 0; i < FN; ++i) vb[i] = scaled(u32x2{x.b[i][c][2 * e], x.b[i][c][2 * e + 1]}, fb);
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-          const bf16x8 va = scaled(u32x2{x.a[j][c][2 * e], x.a[j][c][2 * e + 1]}, scale_float(x.sa[j]));
+          const bf16x8 va = scaled(u32x2{x.a[j][c][2 * e], x.a[j][c][2 * e + 1]}, fa[j]);
 #pragma unroll
           for (int i = 0; i < FN; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb[i], va, acc[j][i], 0, 0, 0);
         }

@@ -572,6 +572,9 @@ cce_status cce_quantize_blocks(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_m
  * CCE_BF16: the same where the shape is small; larger ones run on the matrix
  * cores' 8-bit instructions, whose own sums over 64 products keep about 16
  * bits (measured: 1.5e-5 of the result's norm, 1/100 of the bf16 rounding).
+ * The scales of a and b act together: one that is large beside one that is
+ * small does no harm.  Products of blocks whose two factors together are below
+ * 2^-117 are within 2^-109 (2^-91 beside rows with a factor above 2^119).
  * ---------------------------------------------------------------------- */
 cce_status cce_block_scaled_gemm(cce_ctx* ctx, cce_dtype out_t, const uint8_t* a, cce_mat a_shape,
                                  const uint8_t* a_scales, int64_t ld_a_scales, const uint8_t* b,

@@ -47,3 +47,59 @@ def test_norm_backward_on_two_streams_with_workspaces_of_its_own(ctx, rows, cols
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(dw[i], want[i][1]) and torch.equal(dx[i], want[i][0]), f"step {step}, call {i}"
+
+
+# ---- the 8-bit product -------------------------------------------------------------------
+EVERY_PRODUCT_KERNEL = [(4, 4104, 400), (12, 4100, 272), (12, 8200, 272), (20, 2600, 272), (25, 8210, 272),
+                        (40, 200, 1040), (130, 1000, 1040), (2100, 2060, 272), (4090, 4104, 272)]
+
+
+def _e8(exponents):
+    return (exponents + 127).to(torch.uint8).view(E8).to(DEV)
+
+
+@pytest.mark.parametrize("m,n,k", EVERY_PRODUCT_KERNEL)
+@pytest.mark.parametrize("ot", [BF, F32])
+@pytest.mark.parametrize("scales", ["opposite", "ends"])
+def test_scales_at_the_ends_of_their_range_give_the_product_in_range(ctx, m, n, k, ot, scales):
+    """Scales of a and b up to 2^125 that cancel (opposite), and rows whose two scales together are
+    2^-116 to 2^120 (ends), with values up to 256 in a and down to 2^-9 in b: integers in [-2, 2] or
+    [-1, 1] times one power of two per row, so every sum is exact in fp32 and within its range, in
+    each kernel."""
+    import collective_overlap_amd as cce
+    g = torch.Generator().manual_seed(m + n)
+    kb, nb, top = -(-k // 128), -(-n // 128), 2 if scales == "opposite" else 1
+    a, b = (torch.randint(-top, top + 1, (r, k), generator=g).float().to(DEV) for r in (m, n))
+    if scales == "opposite":
+        column = torch.randint(-125, 126, (1, kb), generator=g)
+        total = torch.randint(-2, 3, (m, 1), generator=g)
+    else:
+        column = torch.randint(-1, 2, (1, kb), generator=g)
+        total = torch.tensor([-116, -100, 0, 100, 120])[torch.randint(0, 5, (m, 1), generator=g)]
+    ea, eb = total - column, column.expand(nb, kb)
+    a, b = (a * (256 / top)).to(E4), (b * 2.0 ** -9).to(E4)
+    c = torch.empty((m, -(-n // 8) * 8), device=DEV, dtype=ot)[:, :n]
+    cce.cce_block_scaled_gemm(ctx, a, _e8(ea), b, _e8(eb), c)
+    want = (a.double() @ b.double().t().contiguous()) * torch.exp2(total.double()).to(DEV)
+    want = want.float().to(ot)
+    assert torch.equal(c, want), f"{int((c != want).sum())} of {want.numel()} differ"
+    if scales == "ends":
+        s = _e8(ea)
+        s.view(torch.uint8)[m // 2, 1] = 255
+        cce.cce_block_scaled_gemm(ctx, a, s, b, _e8(eb), c)
+        other = torch.arange(m, device=DEV) != m // 2
+        assert bool(torch.isnan(c[m // 2]).all()) and torch.equal(c[other], want[other])
+
+
+def test_the_largest_values_times_small_ones(ctx):
+    """bf16's largest value quantises to 256 * 2^120; its product with weights of 2^-100 is in range."""
+    import collective_overlap_amd as cce
+    x = torch.full((3, 256), 3.3895e38, dtype=BF, device=DEV)
+    w = torch.full((128, 256), 2.0 ** -100, device=DEV)
+    q, s = torch.empty((3, 256), device=DEV, dtype=E4), torch.empty((3, 2), device=DEV, dtype=E8)
+    b, t = torch.empty((128, 256), device=DEV, dtype=E4), torch.empty((1, 2), device=DEV, dtype=E8)
+    cce.cce_quantize_blocks(ctx, x, q, s, 1)
+    cce.cce_quantize_blocks(ctx, w, b, t, 128)
+    c = torch.empty((3, 128), device=DEV)
+    cce.cce_block_scaled_gemm(ctx, q, s, b, t, c)
+    assert bool((c == 256 * 2.0 ** 28).all()), c[0, 0].item()
