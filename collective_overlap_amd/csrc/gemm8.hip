@@ -476,7 +476,7 @@ __global__ __launch_bounds__(256) void gemm8_wide_kernel(G8Args a) {
         const int n = n0 + wn * WTN + 32 * i + 8 * q + 4 * h;
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = a.gelu ? gelu_exact(acc[i][j][4 * q + e]) : acc[i][j][4 * q + e];
+        for (int e = 0; e < 4; ++e) v[e] = a.gelu ? gelu_for<TOut>(acc[i][j][4 * q + e]) : acc[i][j][4 * q + e];
         if (n + 4 <= a.N) {       // (16 or 8 bytes, aligned: ldc is a multiple of 8)
           if constexpr (sizeof(TOut) == 4) {
             *reinterpret_cast<f32x4*>(c + n) = f32x4{v[0], v[1], v[2], v[3]};
@@ -615,7 +615,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm8_rows_kernel(G8Args a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int n = n0 + 16 * i + 4 * g + e;
-        const float v = a.gelu ? gelu_exact(acc[j][i][e]) : acc[j][i][e];
+        const float v = a.gelu ? gelu_for<TOut>(acc[j][i][e]) : acc[j][i][e];
         if (n < a.N) c[n] = static_cast<TOut>(v);
       }
     }

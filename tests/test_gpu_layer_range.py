@@ -103,3 +103,25 @@ def test_the_largest_values_times_small_ones(ctx):
     c = torch.empty((3, 128), device=DEV)
     cce.cce_block_scaled_gemm(ctx, q, s, b, t, c)
     assert bool((c == 256 * 2.0 ** 28).all()), c[0, 0].item()
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 4104, 32), (20, 2600, 32), (40, 200, 32), (130, 1000, 32), (2100, 2060, 32)])
+def test_gelu_of_fp32_results_is_fp32(ctx, m, n, k):
+    """Sums that are exact in fp32 (multiples of 1/16, to beyond 6 on both sides), so that the error
+    is GELU's own, relative to the result: the exponent x^2 / 2 is rounded twice, with a factor off
+    by 0.22 u, 1.2 x^2 u; the reciprocal in erfc's argument by 3 u, which counts threefold at x = 0;
+    a polynomial of degree 8 and its coefficients 5 u; the exponential 2 u, the products 3 u.  (An
+    erf good to 1.5e-7 is off by 3e-3, 50000 u, at x = -4.)"""
+    import collective_overlap_amd as cce
+    g = torch.Generator().manual_seed(m)
+    a, b = (torch.randint(-2, 3, (r, k), generator=g).float().to(DEV).to(E4) for r in (m, n))
+    c, y = (torch.empty((m, -(-n // 8) * 8), device=DEV)[:, :n] for _ in range(2))
+    sa, sb = _e8(torch.randint(-4, 1, (m, 1), generator=g)), _e8(torch.zeros(-(-n // 128), 1))
+    cce.cce_block_scaled_gemm(ctx, a, sa, b, sb, c)
+    cce.cce_block_scaled_gemm(ctx, a, sa, b, sb, y, gelu=True)
+    x = c.double()
+    assert torch.equal(x, (a.double() @ b.double().t().contiguous()) * sa.float().double())
+    ref = 0.5 * x * torch.special.erfc(-x * 2 ** -0.5)
+    tol = (1.2 * x * x + 20) * U * ref.abs() + 1e-37
+    bad = ~((y.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), x[bad][0].item(), y[bad][0].item(), ref[bad][0].item())
