@@ -58,7 +58,7 @@ constexpr uint32_t kOob = 0x40000000;      // past every buffer below
 constexpr int kBL = 64;                    // l per tile
 constexpr int kNW = 4;                     // waves (of a group)
 constexpr int kRowWaves = 2;               // waves of a workgroup of ragged_rows_kernel,
-constexpr unsigned kRowGroups = 2048;      // and the most workgroups (4 waves, 1024: 3% slower)
+constexpr int64_t kRowGroups = 2048;       // and the most workgroups (4 waves, 1024: 3% slower)
 constexpr int kGroups = 4;                 // groups of waves where tiles are few
 
 struct RArgs {
@@ -141,7 +141,7 @@ __device__ __forceinline__ int scan_experts(const RArgs& a, F&& f) {
 // walks an expert's tiles in bands of 4 tile rows, so that the tiles in
 // flight share X and Y in the XCD's L2.  false: no tile for this workgroup.
 template <int BM>
-__device__ __forceinline__ bool find_row_tile(const RArgs& a, int w, Tile& t) {
+__device__ __forceinline__ bool find_row_tile(const RArgs& a, int64_t w, Tile& t) {
   // Of up to 64 experts the lanes keep what the scan saw; of more, a second
   // scan finds the tile's.
   int f = 0, n = 0, lo = 0, hi = 0;
@@ -649,8 +649,8 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RArgs a) {
   // (a workgroup takes several tiles, and most tiles that there could be are not
   // there: a workgroup for each of those took 2 to 3 us of 17)
   Tile t;
-  for (int w = blockIdx.x; find_row_tile<16 * FM>(a, w, t); w += gridDim.x) {
-    if (w != static_cast<int>(blockIdx.x)) __syncthreads();   // the last tile's sums are read
+  for (int64_t w = blockIdx.x; find_row_tile<16 * FM>(a, w, t); w += gridDim.x) {
+    if (w != blockIdx.x) __syncthreads();   // the last tile's sums are read
     const int i0 = t.ti * 16 * FM, j0 = t.tj * 16;
     const TileArgs<false, false, TOut> p(a, t, i0, j0);
     const int lane = threadIdx.x & 63;
@@ -772,9 +772,9 @@ hipError_t launch_tiles(RArgs& r, bool f32, hipStream_t s) {
 
 template <int FM>
 hipError_t launch_rows(RArgs& r, bool f32, hipStream_t s) {
-  dim3 grid;
-  if (const hipError_t e = grid_of(r, 1, most_row_tiles(r, 16 * FM), 16, grid); e != hipSuccess) return e;
-  grid.x = std::min(grid.x, kRowGroups);
+  r.tiles_j = (r.J + 15) / 16;
+  const int64_t tiles = (most_row_tiles(r, 16 * FM) * r.tiles_j + 7) / 8 * 8;
+  const dim3 grid(static_cast<unsigned>(std::min(tiles, kRowGroups)));    // (each takes its tiles in turn)
   if (f32) ragged_rows_kernel<FM, kRowWaves, float><<<grid, 64 * kRowWaves, 0, s>>>(r);
   else ragged_rows_kernel<FM, kRowWaves, __bf16><<<grid, 64 * kRowWaves, 0, s>>>(r);
   return hipGetLastError();

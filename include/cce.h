@@ -599,6 +599,9 @@ cce_status cce_block_scaled_gemm(cce_ctx* ctx, cce_dtype out_t, const uint8_t* a
  * The offsets are not known to the host and cannot be refused: those outside
  * [0, T] act as the nearest row number inside, and one that is below its
  * predecessor acts as that (its expert, or the one before, has fewer rows).
+ * CCE_EUNSUPPORTED where the result could have 2^24 tiles or more, of 64 x 64
+ * to 256 x 256 and one row of them more per expert than the rows fill (not with
+ * four rows per expert or fewer on average, forward).
  * ---------------------------------------------------------------------- */
 cce_status cce_ragged_gemm(cce_ctx* ctx, cce_dtype out_t, int n_experts, const int64_t* offsets,
                            const void* a, cce_mat a_shape, const void* b, cce_mat b_shape,

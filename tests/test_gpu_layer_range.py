@@ -125,3 +125,21 @@ def test_gelu_of_fp32_results_is_fp32(ctx, m, n, k):
     tol = (1.2 * x * x + 20) * U * ref.abs() + 1e-37
     bad = ~((y.double() - ref).abs() <= tol)
     assert not bool(bad.any()), (int(bad.sum()), x[bad][0].item(), y[bad][0].item(), ref[bad][0].item())
+
+
+# ---- the products grouped by expert --------------------------------------------------------
+def test_few_rows_of_many_experts_times_a_wide_shared_matrix(ctx):
+    """1024 rows of 256 experts and 2^20 columns: 20 million tiles that there could be, for a grid
+    that takes them in turn.  One matrix for all experts, so one product is the reference."""
+    import collective_overlap_amd as cce
+    rows, n, k, experts = 1024, 1 << 20, 16, 256
+    g = torch.Generator(device=DEV).manual_seed(1)
+    a = torch.randint(-3, 4, (rows, k), generator=g, device=DEV).to(BF)
+    w = torch.randint(-3, 4, (n, k), generator=g, device=DEV).to(BF)
+    off = torch.arange(experts + 1, device=DEV) * 4
+    off[1:9] = torch.tensor([0, 1, 1, 20, 20, 21, 25, 32], device=DEV)
+    c = torch.full((rows, n), 5.0, device=DEV, dtype=BF)
+    cce.cce_ragged_gemm(ctx, a, w.expand(experts, n, k), off, c)
+    wt = w.float().t().contiguous()
+    for i in range(0, rows, 128):
+        assert torch.equal(c[i:i + 128], (a[i:i + 128].float() @ wt).to(BF)), f"rows from {i}"
