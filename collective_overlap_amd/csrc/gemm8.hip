@@ -657,7 +657,8 @@ cce_status launch_gemm8(const Gemm8Launch& L, void* stream) {
            static_cast<int>(L.ld_sb), L.gelu,
            ((reinterpret_cast<uintptr_t>(L.sa) | reinterpret_cast<uintptr_t>(L.sb) | L.ld_sa | L.ld_sb) & 3) == 0};
   auto tiles = [&](int64_t b) { return ((L.M + b - 1) / b) * ((L.N + b - 1) / b); };
-  if (tiles(64) > 0xffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
+  // (128 x 128 are the smallest where there are many; a launch has fewer than 2^32 threads)
+  if (tiles(128) > 0xffffff) return fail(CCE_EUNSUPPORTED, "block-scaled GEMM: too many output tiles");
   const bool f32 = L.out_t == CCE_F32;
   // Few rows, or so few 64 x 64 tiles that a tile's length in K is the time
   // (64 x 64 x 8192: 11 us against 27; 130 x 520 x 4096: 13 against 15).  Up to

@@ -568,6 +568,7 @@ cce_status cce_quantize_blocks(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_m
  * Product of two 8-bit matrices in blocks: c = a * b^T with a [M, K] in
  * 1 x 128 blocks and b^T [N, K] in 128 x 128 blocks, c [M, N] of out_t.
  * K and the ld of a and b are multiples of 16.  flags: CCE_FLAG_GELU.
+ * CCE_EUNSUPPORTED for 2^24 tiles of 128 x 128 results or more.
  * out_t CCE_F32: every product is exact and sums are in fp32.  out_t
  * CCE_BF16: the same where the shape is small; larger ones run on the matrix
  * cores' 8-bit instructions, whose own sums over 64 products keep about 16

@@ -143,3 +143,22 @@ def test_few_rows_of_many_experts_times_a_wide_shared_matrix(ctx):
     wt = w.float().t().contiguous()
     for i in range(0, rows, 128):
         assert torch.equal(c[i:i + 128], (a[i:i + 128].float() @ wt).to(BF)), f"rows from {i}"
+
+
+@pytest.mark.parametrize("ot", [BF, F32])
+def test_product_of_the_most_rows(ctx, ot):
+    """2^30 rows, the documented most, of 16 and 8 columns."""
+    import collective_overlap_amd as cce
+    m, n, k = 1 << 30, 8, 16
+    pick = torch.tensor([0, 255, 256, (1 << 29) + 1, (1 << 30) - 257, (1 << 30) - 1], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    a = torch.zeros((m, k), device=DEV, dtype=torch.uint8).view(E4)
+    some = torch.randint(-3, 4, (len(pick), k), generator=g, device=DEV).float()
+    a.view(torch.uint8)[pick] = some.to(E4).view(torch.uint8)
+    b = torch.randint(1, 4, (n, k), generator=g, device=DEV).float()
+    s = torch.full((m, 1), 127, device=DEV, dtype=torch.uint8).view(E8)
+    c = torch.empty((m, n), device=DEV, dtype=ot)
+    cce.cce_block_scaled_gemm(ctx, a, s, b.to(E4), _e8(torch.zeros(1, 1)), c)
+    want = (some.double() @ b.double().t().contiguous()).to(ot)
+    assert torch.equal(c[pick], want)
+    assert sum(int(torch.count_nonzero(x)) for x in c.split(1 << 26)) == int(torch.count_nonzero(want))
