@@ -20,11 +20,16 @@ struct e4m3 {          // one byte of OCP E4M3 (finite, NaN 0x7f / 0xff, no infi
 
 constexpr int kScaleCols = 128;   // columns that share a scale
 
+// Column j of a row of n columns lies before its end.  Unsigned, and so the sums
+// and products that give j: the last lanes' columns may lie past 2^31, where n
+// is close to it.
+__device__ __forceinline__ bool before(uint32_t j, int n) { return j < static_cast<uint32_t>(n); }
+
 // Columns [j, j + 8) of a row at `base` (16-byte aligned with j a multiple of
 // 8); columns from n on read as zero.  NT: streamed past the caches.
 template <typename T, bool NT = false>
-__device__ __forceinline__ void load8(const T* base, int j, int n, float (&v)[8]) {
-  if (j + 8 <= n) {
+__device__ __forceinline__ void load8(const T* base, uint32_t j, int n, float (&v)[8]) {
+  if (before(j + 7, n)) {
     if constexpr (sizeof(T) == 4) {
       const f32x4* p = reinterpret_cast<const f32x4*>(base + j);
       const f32x4 x = NT ? __builtin_nontemporal_load(p) : p[0];
@@ -42,14 +47,14 @@ __device__ __forceinline__ void load8(const T* base, int j, int n, float (&v)[8]
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = j + e < n ? static_cast<float>(base[j + e]) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = before(j + e, n) ? static_cast<float>(base[j + e]) : 0.0f;
   }
 }
 
 // One rounding to T (to nearest even), columns from n on left alone.
 template <typename T>
-__device__ __forceinline__ void store8(T* base, int j, int n, const float (&v)[8]) {
-  if (j + 8 <= n) {
+__device__ __forceinline__ void store8(T* base, uint32_t j, int n, const float (&v)[8]) {
+  if (before(j + 7, n)) {
     if constexpr (sizeof(T) == 4) {
       f32x4* p = reinterpret_cast<f32x4*>(base + j);
       __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, p);
@@ -63,12 +68,12 @@ __device__ __forceinline__ void store8(T* base, int j, int n, const float (&v)[8
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (j + e < n) base[j + e] = static_cast<T>(v[e]);
+      if (before(j + e, n)) base[j + e] = static_cast<T>(v[e]);
   }
 }
 
 // 8 values to e4m3, each rounded to nearest even.
-__device__ __forceinline__ void store8_e4m3(uint8_t* base, int j, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8_e4m3(uint8_t* base, uint32_t j, int n, const float (&v)[8]) {
   u32x2 w;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -76,12 +81,12 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* base, int j, int n, const f
     p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], p, true);
     w[h] = static_cast<unsigned>(p);
   }
-  if (j + 8 <= n) {
+  if (before(j + 7, n)) {
     __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(base + j));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (j + e < n) base[j + e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
+      if (before(j + e, n)) base[j + e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
   }
 }
 

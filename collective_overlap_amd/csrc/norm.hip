@@ -68,7 +68,7 @@ __device__ __forceinline__ float rstd_of(double squares, int cols, float eps) {
   return r > 0.0 ? static_cast<float>(r * (1.5 - 0.5 * x * r * r)) : static_cast<float>(r);
 }
 
-__device__ __forceinline__ void load_weight(const NArgs& a, int j, float (&w)[8]) {
+__device__ __forceinline__ void load_weight(const NArgs& a, uint32_t j, float (&w)[8]) {
   if (a.w_f32) load8(reinterpret_cast<const float*>(a.w), j, a.cols, w);
   else load8(reinterpret_cast<const __bf16*>(a.w), j, a.cols, w);
 }
@@ -143,7 +143,7 @@ __device__ __forceinline__ void widen(const Raw<T>& x, int j, int n, float (&v)[
 }
 
 template <typename TX>
-__device__ __forceinline__ void load_sum(const NArgs& a, int64_t row, int j, float (&v)[8]) {
+__device__ __forceinline__ void load_sum(const NArgs& a, int64_t row, uint32_t j, float (&v)[8]) {
   load8(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, v);
   if (a.res) {
     float r[8];
@@ -158,24 +158,24 @@ __device__ __forceinline__ void load_sum(const NArgs& a, int64_t row, int j, flo
 template <typename TO>
 __device__ __forceinline__ void finish(const NArgs& a, int64_t row, int i, const float (&v)[8], const float (&w)[8],
                                        float rstd) {
-  const int j = 8 * i;
+  const uint32_t j = 8u * i;
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = v[e] * rstd * w[e];
   if constexpr (sizeof(TO) == 1) {
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, j + e < a.cols ? magnitude(y[e]) : 0u);
+    for (int e = 0; e < 8; ++e) top = max(top, before(j + e, a.cols) ? magnitude(y[e]) : 0u);
     const uint32_t s = scale_of(max16(top));
     const float inv = inverse_of(s);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] *= inv;
-    if (j < a.cols) {
+    if (before(j, a.cols)) {
       store8_e4m3(reinterpret_cast<uint8_t*>(a.out) + row * a.ld_out, j, a.cols, y);
       if (i % 16 == 0) a.scales[row * a.ld_scales + i / 16] = static_cast<uint8_t>(s);
     }
   } else {
-    if (j < a.cols) store8(reinterpret_cast<TO*>(a.out) + row * a.ld_out, j, a.cols, y);
+    if (before(j, a.cols)) store8(reinterpret_cast<TO*>(a.out) + row * a.ld_out, j, a.cols, y);
   }
 }
 
@@ -300,8 +300,8 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_wide_kernel(NArgs a) {
     const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
     for (int i0 = 0; i0 < vectors; i0 += kThreads) {   // (every lane: a scale's maximum needs its 16)
       float v[8], w[8];
-      load_sum<TX>(a, row, 8 * (i0 + tid), v);
-      load_weight(a, 8 * (i0 + tid), w);
+      load_sum<TX>(a, row, 8u * (i0 + tid), v);
+      load_weight(a, 8u * (i0 + tid), w);
       finish<TO>(a, row, i0 + tid, v, w, rstd);
     }
   }
@@ -535,11 +535,11 @@ template <typename TX>
 __global__ __launch_bounds__(kThreads) void rmsnorm_dweight_kernel(BArgs a) {
   __shared__ float sh[4][64 * 8 + 4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j = (blockIdx.x * 64 + lane) * 8;
+  const uint32_t j = (blockIdx.x * 64 + lane) * 8;
   const int64_t per = (a.rows + a.chunks - 1) / a.chunks;
   const int64_t r0 = blockIdx.y * per, r1 = min(r0 + per, static_cast<int64_t>(a.rows));
   float s[8] = {};
-  if (j < a.cols) {
+  if (before(j, a.cols)) {
     for (int64_t row = r0 + wave; row < r1; row += 4) {
       float v[8], d[8];
       load8(reinterpret_cast<const TX*>(a.x) + row * a.ld_x, j, a.cols, v);
@@ -552,11 +552,11 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_dweight_kernel(BArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) sh[wave][lane * 8 + e] = s[e];
   __syncthreads();
-  if (wave == 0 && j < a.cols) {
+  if (wave == 0 && before(j, a.cols)) {
     float* p = a.part + static_cast<int64_t>(blockIdx.y) * a.ld_part + j;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (j + e < a.cols)
+      if (before(j + e, a.cols))
         p[e] = sh[0][lane * 8 + e] + sh[1][lane * 8 + e] + sh[2][lane * 8 + e] + sh[3][lane * 8 + e];
   }
 }
@@ -587,6 +587,7 @@ struct QArgs {
   uint8_t* scales;
   int rows, cols;
   int64_t ld_x, ld_q, ld_scales;
+  int64_t block0;      // first block of the launch (128 x 128)
 };
 
 // Blocks of 1 x 128: 16 lanes per block.  TPR threads side by side take 8 TPR
@@ -596,11 +597,11 @@ constexpr int kRowsEach = 2;
 template <typename TX, int TPR>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QArgs a) {
   constexpr int RPW = kThreads / TPR;
-  const int chunks = (a.cols + 8 * TPR - 1) / (8 * TPR);
+  const int chunks = (a.cols + 8u * TPR - 1) / (8 * TPR);
   const int64_t total = (a.rows + int64_t{RPW} * kRowsEach - 1) / (RPW * kRowsEach) * chunks;
   for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {   // (more than once only in a grid of the most workgroups)
     const int group = static_cast<int>(b / chunks), chunk = static_cast<int>(b - static_cast<int64_t>(group) * chunks);
-    const int j = chunk * 8 * TPR + 8 * (threadIdx.x % TPR);
+    const uint32_t j = chunk * 8u * TPR + 8 * (threadIdx.x % TPR);
     const int64_t row0 = static_cast<int64_t>(group) * RPW * kRowsEach + threadIdx.x / TPR;
     float v[kRowsEach][8];
 #pragma unroll
@@ -623,7 +624,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QArgs a) {
       const float inv = inverse_of(s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[u][e] *= inv;
-      if (row < a.rows && j < a.cols) {
+      if (row < a.rows && before(j, a.cols)) {
         store8_e4m3(a.q + row * a.ld_q, j, a.cols, v[u]);
         if ((j & (kScaleCols - 1)) == 0) a.scales[row * a.ld_scales + j / kScaleCols] = static_cast<uint8_t>(s);
       }
@@ -638,10 +639,10 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QArgs a) {
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(QArgs a) {
   __shared__ uint32_t sh[kThreads / 64];
-  const int blocks = (a.cols + kScaleCols - 1) / kScaleCols;
-  const int64_t br = blockIdx.x / blocks;          // block row and column
-  const int bc = static_cast<int>(blockIdx.x - br * blocks);
-  const int j = bc * kScaleCols + 8 * (threadIdx.x & 15);
+  const int blocks = (a.cols + kScaleCols - 1u) / kScaleCols;
+  const int64_t b = a.block0 + blockIdx.x, br = b / blocks;          // block row and column
+  const int bc = static_cast<int>(b - br * blocks);
+  const uint32_t j = bc * static_cast<uint32_t>(kScaleCols) + 8 * (threadIdx.x & 15);
   const int64_t row0 = br * 128 + (threadIdx.x >> 4);
   float v[8][8];
 #pragma unroll
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tiles_kernel(QArgs a) {
     const int64_t row = row0 + 16 * u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[u][e] *= inv;
-    if (row < a.rows && j < a.cols) store8_e4m3(a.q + row * a.ld_q, j, a.cols, v[u]);
+    if (row < a.rows && before(j, a.cols)) store8_e4m3(a.q + row * a.ld_q, j, a.cols, v[u]);
   }
   if (threadIdx.x == 0) a.scales[br * a.ld_scales + bc] = static_cast<uint8_t>(s);
 }
@@ -836,16 +837,18 @@ cce_status launch_rmsnorm_backward(const NormBackwardLaunch& L, void* stream) {
     }
   }
   if (!L.dw) return CCE_OK;
-  column_sum_kernel<<<dim3(static_cast<unsigned>((L.cols + 15) / 16)), kThreads, 0, s>>>(a.part, a.chunks, a.ld_part,
-                                                                                       a.dw, a.cols);
+  for (int64_t c = 0; c < L.cols; c += 16 * kMaxGrid)
+    column_sum_kernel<<<grid_for((L.cols - c + 15) / 16), kThreads, 0, s>>>(a.part + c, a.chunks, a.ld_part, a.dw + c,
+                                                                           static_cast<int>(L.cols - c));
   return launched("rmsnorm weight gradient sum");
 }
 
 template <typename TX>
-void launch_quantize(const QArgs& a, int block_rows, hipStream_t s) {
+void launch_quantize(QArgs a, int block_rows, hipStream_t s) {
   if (block_rows == 128) {
     const int64_t blocks = ((a.cols + int64_t{127}) / 128) * ((a.rows + int64_t{127}) / 128);
-    quantize_tiles_kernel<TX><<<dim3(static_cast<unsigned>(blocks)), kThreads, 0, s>>>(a);
+    for (; a.block0 < blocks; a.block0 += kMaxGrid)
+      quantize_tiles_kernel<TX><<<grid_for(blocks - a.block0), kThreads, 0, s>>>(a);
     return;
   }
   auto go = [&](auto tpr) {
@@ -861,7 +864,7 @@ void launch_quantize(const QArgs& a, int block_rows, hipStream_t s) {
 
 cce_status launch_quantize_blocks(const QuantizeLaunch& L, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  QArgs a{L.x, L.q, L.scales, static_cast<int>(L.rows), static_cast<int>(L.cols), L.ld_x, L.ld_q, L.ld_scales};
+  QArgs a{L.x, L.q, L.scales, static_cast<int>(L.rows), static_cast<int>(L.cols), L.ld_x, L.ld_q, L.ld_scales, 0};
   if (L.x_t == CCE_F32) launch_quantize<float>(a, L.block_rows, s);
   else launch_quantize<__bf16>(a, L.block_rows, s);
   return launched("quantize");

@@ -162,3 +162,47 @@ def test_product_of_the_most_rows(ctx, ot):
     want = (some.double() @ b.double().t().contiguous()).to(ot)
     assert torch.equal(c[pick], want)
     assert sum(int(torch.count_nonzero(x)) for x in c.split(1 << 26)) == int(torch.count_nonzero(want))
+
+
+# ---- the row-wise operators ------------------------------------------------------------------
+@pytest.mark.parametrize("cols", [(1 << 31) - 8, (1 << 31) - 131])
+def test_one_row_of_nearly_two_to_the_31_columns(ctx, cols):
+    """The widest row that can be asked for: the last lanes' columns pass 2^31.  Zeros but for a few
+    columns, so that the sums are exact: the norm's error is that of its root and products."""
+    import collective_overlap_amd as cce
+    pick = torch.tensor([0, 7, 8, 4097, (1 << 30) - 1, 1 << 30, cols - 2050, cols - 9, cols - 1], device=DEV)
+    v = 2.0 ** torch.arange(9, dtype=torch.float64)
+    v = v * torch.tensor([1, -1, 1, 1, -1, 1, -1, 1, 1])
+    def row(dtype):
+        return torch.zeros((1, (1 << 31) - 8), device=DEV, dtype=torch.uint8).view(dtype)[:, :cols] if dtype == E4 else \
+            torch.zeros((1, (1 << 31) - 8), device=DEV, dtype=dtype)[:, :cols]
+    x = row(BF)
+    x[0, pick] = v.to(BF).to(DEV)
+    rstd = 1 / np.sqrt(float((v * v).sum()) / cols + EPS)
+    for br in (1, 128):
+        q, s = row(E4), torch.zeros((1, -(-cols // 128)), device=DEV, dtype=torch.uint8).view(E8)
+        cce.cce_quantize_blocks(ctx, x, q, s, br)
+        got = q[0, pick].float().double().cpu() * s[0, pick // 128].float().double().cpu()
+        assert torch.equal(got, v), (br, got)
+        assert int(torch.count_nonzero(q.view(torch.uint8))) == len(pick)
+        del q, s
+    w = torch.ones((1 << 31) - 8, device=DEV, dtype=BF)[:cols]
+    out = row(BF)
+    cce.cce_rmsnorm(ctx, x, w, out, EPS)
+    within(f64(out[0, pick]), (v * rstd).numpy(), (2.0 ** -8 + 8 * U) * np.abs((v * rstd).numpy()), "out")
+    assert int(torch.count_nonzero(out)) == len(pick)
+    q, s = row(E4), torch.zeros((1, -(-cols // 128)), device=DEV, dtype=torch.uint8).view(E8)
+    cce.cce_rmsnorm(ctx, x, w, q, EPS, scales=s)
+    got = q[0, pick].float().double().cpu().numpy() * s[0, pick // 128].float().double().cpu().numpy()
+    within(got, (v * rstd).numpy(), (2.0 ** -4 + 8 * U) * np.abs((v * rstd).numpy()), "e4m3")
+    assert int(torch.count_nonzero(q.view(torch.uint8))) == len(pick)
+    del q, s
+    # dout = x: the mean of w dout n and n are exact but for the root; dweight = x n
+    dx, dw = out, torch.full((cols,), 3.0, device=DEV)
+    cce.cce_rmsnorm_backward(ctx, x, w, x, dx, dw, EPS)
+    n = (v * rstd).numpy()
+    mean = float((v.numpy() * n).sum()) / cols
+    mag = (np.abs(v.numpy()) + np.abs(n) * mean) * rstd
+    within(f64(dx[0, pick]), (v.numpy() - n * mean) * rstd, (2.0 ** -8 + 24 * U) * mag, "dx")
+    within(f64(dw[pick]), v.numpy() * n, 12 * U * np.abs(v.numpy() * n), "dweight")
+    assert int(torch.count_nonzero(dw)) == len(pick) and int(torch.count_nonzero(dx)) == len(pick)
