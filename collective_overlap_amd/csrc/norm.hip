@@ -327,7 +327,10 @@ struct BArgs {
 // two sums and its dx, and a thread keeps the sums of its columns of dw over
 // the rows its workgroup takes (every gridDim.x-th group of RPW); they go to
 // the workspace at the end, a line per group of threads, and column_sum_kernel
-// adds the lines in their order.  Bound by HBM: 8192 x 12288 bf16 146 us, 5.5
+// adds the lines in their order.  Where the sum of squares passes fp32's range,
+// 1 / root is 0 and so is n, but the sum of w dy x may pass it too: 0 times that
+// is no mean, so the sum of w dy n is formed as it stands (0, or NaN where x is
+// infinite).  Bound by HBM: 8192 x 12288 bf16 146 us, 5.5
 // TB/s (two passes and a third for dw: 267; without the loads ahead: 171).
 template <typename TX, typename TW, int THREADS, int RPW, int NV>
 __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
@@ -390,7 +393,25 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
       __builtin_amdgcn_sched_barrier(0);   // (one vector widened at a time)
     }
     const float rstd = rstd_of(row_sum<TPR / 64>(ss, sh), a.cols, a.eps);
-    const float mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;   // of w dy n
+    float mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;   // of w dy n
+    if (rstd == 0.0f) {
+      dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int j = 8 * (t + i * TPR);
+        float v[8], g[8], u[8];
+        widen(x[i], j, a.cols, v);
+        widen(d[i], j, a.cols, g);
+        widen(w[i], j, a.cols, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += g[e] * u[e] * (v[e] * rstd);
+        keep_raw(x[i]);
+        keep_raw(d[i]);
+        keep_raw(w[i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mean = static_cast<float>(row_sum<TPR / 64>(dot, sh2));
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = 8 * (t + i * TPR);
@@ -461,7 +482,14 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_narrow_kernel(BArgs
       dot += q.d[e] * w[e] * q.x[e];
     }
     const float rstd = rstd_of(lane_sum<TPR>(ss), a.cols, a.eps);
-    const float mean = static_cast<float>(lane_sum<TPR>(dot) * (1.0 / a.cols)) * rstd;   // of w dy n
+    float mean = static_cast<float>(lane_sum<TPR>(dot) * (1.0 / a.cols)) * rstd;   // of w dy n
+    if (__any(rstd == 0.0f)) {      // (as above; the wave's other rows keep theirs)
+      dot = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dot += q.d[e] * w[e] * (q.x[e] * rstd);
+      const float zero = static_cast<float>(lane_sum<TPR>(dot));
+      if (rstd == 0.0f) mean = zero;
+    }
     float g[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -509,7 +537,19 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
       }
     }
     const float rstd = rstd_of(row_sum<kThreads / 64>(ss, sh), a.cols, a.eps);
-    const float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;
+    float mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2) * (1.0 / a.cols)) * rstd;
+    if (rstd == 0.0f) {      // (as above)
+      dot = 0.0f;
+      for (int i = tid; i < vectors; i += kThreads) {
+        float v[8], d[8], w[8];
+        load8(x, 8 * i, a.cols, v);
+        load8(dy, 8 * i, a.cols, d);
+        load_weight(wa, 8 * i, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot += d[e] * w[e] * (v[e] * rstd);
+      }
+      mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2));
+    }
     if (tid == 0) a.rstd[row] = rstd;
     for (int i = tid; i < vectors; i += kThreads) {
       float v[8], d[8], w[8], g[8];

@@ -540,6 +540,8 @@ cce_status cce_rmsnorm(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_mat x_sha
  *   dweight = sum over the rows of dout n
  * d_residual (NULL: none) is the gradient that reached residual_out on its
  * other path.  Because r = x + residual, dx is the gradient of both.
+ * (A row whose sum of squares passes fp32's range, as its norm of zero, passes
+ * no gradient on: dx is d_residual there, and it adds nothing to dweight.)
  * x, dout, d_residual and dx are of x_t; weight of weight_t; dweight [cols]
  * is fp32 (NULL: not wanted; zeros when there are no rows).  All sums are in
  * fp32 and in a fixed order.  workspace: device memory of the size the query

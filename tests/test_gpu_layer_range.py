@@ -206,3 +206,43 @@ def test_one_row_of_nearly_two_to_the_31_columns(ctx, cols):
     within(f64(dx[0, pick]), (v.numpy() - n * mean) * rstd, (2.0 ** -8 + 24 * U) * mag, "dx")
     within(f64(dw[pick]), v.numpy() * n, 12 * U * np.abs(v.numpy() * n), "dweight")
     assert int(torch.count_nonzero(dw)) == len(pick) and int(torch.count_nonzero(dx)) == len(pick)
+
+
+@pytest.mark.parametrize("cols", [40, 128, 200, 600, 1000, 2000, 4096, 8000, 12288, 16392])
+@pytest.mark.parametrize("xt", [BF, F32])
+@pytest.mark.parametrize("d_residual", [False, True])
+def test_norm_backward_of_overflowing_infinite_and_nan_rows(ctx, cols, xt, d_residual):
+    """A row whose squares pass fp32's range has a norm of zero, so no gradient passes it, also
+    where the sum of w dout x overflows; a row with an infinity has n = NaN there and 0 elsewhere,
+    so its mean and its dx are NaN, and dweight in that column; a NaN makes the row NaN, and
+    dweight.  Other rows keep theirs."""
+    import collective_overlap_amd as cce
+    rows = 70
+    x, d = randn((rows, cols), 1, 1, xt), randn((rows, cols), 2, 1, xt)
+    x[3] = 3e38 * torch.sign(x[3]) * (1 if xt == F32 else 0.99)
+    d[3] = 1e30 * torch.sign(x[3])
+    x[37] = 1e25
+    x[41, cols // 2] = float("inf")
+    w = (1 + randn((cols,), 3, 0.2)).to(DEV)
+    r = randn((rows, cols), 4, 1, xt).to(DEV) if d_residual else None
+    dx, dw = torch.empty((rows, cols), device=DEV, dtype=xt), torch.empty(cols, device=DEV)
+    cce.cce_rmsnorm_backward(ctx, x.to(DEV), w, d.to(DEV), dx, dw, EPS, d_residual=r)
+    for i in (3, 37):
+        assert torch.equal(dx[i], r[i] if d_residual else torch.zeros_like(dx[i])), i
+    assert bool(torch.isnan(dx[41]).all())
+    other = [i for i in range(rows) if i not in (3, 37, 41)]
+    ref, _ = ol.rmsnorm_backward(f64(x[other]), f64(w), f64(d[other]), EPS, None if r is None else f64(r[other]))
+    got = f64(dx[other])
+    assert np.linalg.norm(got - ref) <= (HALF[xt] + 4 * cols * U) * np.linalg.norm(ref)
+    column = torch.arange(cols, device=DEV) == cols // 2
+    assert bool(torch.isnan(dw[column]).all())
+    some = [i for i in range(rows) if i != 41]
+    x64 = f64(x)
+    x64[[3, 37]] = 0.0
+    _, refw = ol.rmsnorm_backward(x64[some], f64(w), np.where(np.abs(f64(d[some])) > 1e29, 0, f64(d[some])), EPS)
+    keep = ~column.cpu().numpy()
+    assert np.linalg.norm((f64(dw) - refw)[keep]) <= 1e-5 * np.linalg.norm(refw[keep])
+    x[41, cols // 2], x[5, 1] = 1.0, float("nan")
+    cce.cce_rmsnorm_backward(ctx, x.to(DEV), w, d.to(DEV), dx, dw, EPS, d_residual=r)
+    bad = torch.isnan(dx).any(1).cpu()
+    assert bool(torch.isnan(dx[5]).all()) and int(bad.sum()) == 1 and bool(torch.isnan(dw).all())
