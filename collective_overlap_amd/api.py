@@ -533,7 +533,7 @@ def cce_rmsnorm(ctx: Context, x, weight, out, eps: float = 1e-5, residual=None, 
 
 
 def cce_rmsnorm_backward_workspace(shape) -> int:
-    """shape: (rows, cols)."""
+    """shape: (rows, cols).  Only a call with dweight uses it."""
     nb = ctypes.c_size_t()
     check(lib().cce_rmsnorm_backward_workspace(cce_mat(shape[0], shape[1], -(-shape[1] // 8) * 8),
                                                ctypes.byref(nb)), "cce_rmsnorm_backward_workspace")
@@ -552,8 +552,8 @@ def cce_rmsnorm_backward(ctx: Context, x, weight, dout, dx, dweight=None, eps: f
     if dweight is not None:
         _vector(dweight, cols, "dweight", torch.float32)
     _on_device(ctx, (x, weight, dout, dx, dweight, d_residual, workspace))
-    ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(shape), dx.device, workspace,
-                         stream)
+    ws, wsb = _workspace(lambda: cce_rmsnorm_backward_workspace(shape) if dweight is not None else 0,
+                         dx.device, workspace, stream)
     check(lib().cce_rmsnorm_backward(
         ctx.handle, _dtype(dtype), x.data_ptr(), cce_mat(rows, cols, ld), weight.data_ptr(),
         _dtype(weight.dtype), dout.data_ptr(), ld_d, _ptr(d_residual), ld_r, float(eps), dx.data_ptr(),

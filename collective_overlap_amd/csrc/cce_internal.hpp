@@ -172,7 +172,7 @@ struct NormBackwardLaunch {
   const void* dres = nullptr;     // NULL: none
   void* dx = nullptr;
   float* dw = nullptr;            // NULL: not wanted
-  void* workspace = nullptr;      // rmsnorm_backward_bytes
+  void* workspace = nullptr;      // rmsnorm_backward_bytes; unused without dw
   int64_t rows = 0, cols = 0, ld_x = 0, ld_dout = 0, ld_dres = 0, ld_dx = 0;   // rows may be 0: dw = 0
   float eps = 0;
 };

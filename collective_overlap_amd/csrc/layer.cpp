@@ -266,7 +266,7 @@ cce_status cce_rmsnorm_backward(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_
     if (d_residual) CCE_TRY(check_operand("d_residual", d_residual, rm, rs));
     CCE_TRY(check_operand("dx", dx, om, os));
     CCE_TRY(check_ptr("dweight", dweight, dws));
-    const size_t need = rmsnorm_backward_bytes(rows, cols);
+    const size_t need = dweight ? rmsnorm_backward_bytes(rows, cols) : 0;   // (all of it is for dweight)
     if (need > 0 && (!workspace || workspace_bytes < need))
       return fail(CCE_EWORKSPACE, "workspace: " + std::to_string(need) + " bytes needed");
     if (need > 0) CCE_TRY(check_ptr("workspace", workspace, static_cast<int64_t>(need)));

@@ -550,7 +550,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_wide_kernel(BArgs a
       }
       mean = static_cast<float>(row_sum<kThreads / 64>(dot, sh2));
     }
-    if (tid == 0) a.rstd[row] = rstd;
+    if (a.dw && tid == 0) a.rstd[row] = rstd;
     for (int i = tid; i < vectors; i += kThreads) {
       float v[8], d[8], w[8], g[8];
       load8(x, 8 * i, a.cols, v);

@@ -545,7 +545,8 @@ cce_status cce_rmsnorm(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_mat x_sha
  * x, dout, d_residual and dx are of x_t; weight of weight_t; dweight [cols]
  * is fp32 (NULL: not wanted; zeros when there are no rows).  All sums are in
  * fp32 and in a fixed order.  workspace: device memory of the size the query
- * returns, 16-byte aligned; its contents on entry do not matter.
+ * returns, 16-byte aligned; its contents on entry do not matter.  Without
+ * dweight none is used and it may be NULL.
  * ---------------------------------------------------------------------- */
 cce_status cce_rmsnorm_backward_workspace(cce_mat x_shape, size_t* bytes);
 

@@ -246,3 +246,17 @@ def test_norm_backward_of_overflowing_infinite_and_nan_rows(ctx, cols, xt, d_res
     cce.cce_rmsnorm_backward(ctx, x.to(DEV), w, d.to(DEV), dx, dw, EPS, d_residual=r)
     bad = torch.isnan(dx).any(1).cpu()
     assert bool(torch.isnan(dx[5]).all()) and int(bad.sum()) == 1 and bool(torch.isnan(dw).all())
+
+
+@pytest.mark.parametrize("rows,cols", [(300, 100), (40, 700), (30, 4104), (20, 16400)])
+def test_norm_backward_without_the_weight_gradient_allocates_nothing(ctx, rows, cols):
+    import collective_overlap_amd as cce
+    x, d, dx, dx2 = (randn((rows, -(-cols // 8) * 8), s, 1, BF).to(DEV)[:, :cols] for s in range(4))
+    w, dw = torch.ones(cols, device=DEV), torch.empty(cols, device=DEV)
+    cce.cce_rmsnorm_backward(ctx, x, w, d, dx2, dw, EPS)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    cce.cce_rmsnorm_backward(ctx, x, w, d, dx, None, EPS)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() == before and torch.equal(dx, dx2)

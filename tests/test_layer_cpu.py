@@ -268,3 +268,10 @@ def test_nothing_to_do_is_ok(L):
     assert _call(L.cce_quantize_blocks, QUANT, QUANT_BASE, dict(xm=cce_mat(0, 64, 64))) == 0
     assert _call(L.cce_block_scaled_gemm, G8, G8_BASE, dict(am=cce_mat(0, 256, 256), cm=cce_mat(0, 8, 8))) == 0
     assert _call(L.cce_ragged_gemm, RAG, RAG_BASE, dict(m0=cce_mat(0, 32, 32), m2=cce_mat(0, 16, 16))) == 0
+
+
+def test_norm_backward_without_the_weight_gradient_needs_no_workspace(L):
+    """The call gets past the workspace's check, to that of the overlap."""
+    for ws, wsb in ((None, 0), (6 * P, 16)):
+        assert _call(L.cce_rmsnorm_backward, BWD, BWD_BASE, dict(dw=None, ws=ws, wsb=wsb, dx=P)) == EINVAL
+        assert _call(L.cce_rmsnorm_backward, BWD, BWD_BASE, dict(ws=ws, wsb=wsb, dx=P)) == EWS
