@@ -260,3 +260,81 @@ def test_norm_backward_without_the_weight_gradient_allocates_nothing(ctx, rows, 
     cce.cce_rmsnorm_backward(ctx, x, w, d, dx, None, EPS)
     torch.cuda.synchronize()
     assert torch.cuda.max_memory_allocated() == before and torch.equal(dx, dx2)
+
+
+# ---- the kernels for large products, on values as they come ----------------------------------
+def _quantised(ctx, rows, cols, block_rows, pad, value):
+    """Quantised by the call under test elsewhere, inside wider storage full of NaN."""
+    import collective_overlap_amd as cce
+    x = torch.empty((rows, -(-cols // 8) * 8), device=DEV)[:, :cols].copy_(value.to(DEV))
+    q = Padded(rows, cols, E4, pad, 16)
+    s = Padded(-(-rows // block_rows), -(-cols // 128), E8, 3, 1)
+    cce.cce_quantize_blocks(ctx, x, q.t, s.t, block_rows)
+    wide = s.t.float().double().repeat_interleave(block_rows, 0)[:rows].repeat_interleave(128, 1)[:, :cols]
+    return q, s, q.t.float().double() * wide
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 1030, 400), (2000, 1100, 4240), (4090, 4104, 272), (5000, 3600, 1040)])
+@pytest.mark.parametrize("gelu", [False, True])
+def test_large_products_of_uneven_values(ctx, m, n, k, gelu):
+    """128 x 128 and 256 x 256 tiles of the 8-bit instruction: what it leaves out of its sums of 64
+    products is at most 2^-12 of the sum of their magnitudes (test_gpu_layer.py), GELU has a slope
+    of at most 1.13 and is off by 4e-7 |c|, and the result is rounded to bf16."""
+    import collective_overlap_amd as cce
+    a, sa, wa = _quantised(ctx, m, k, 1, 16, uneven(m, k, m, F32))
+    b, sb, wb = _quantised(ctx, n, k, 128, 32, randn((n, k), n, 0.05))
+    c = Padded(m, n, BF, 8)
+    cce.cce_block_scaled_gemm(ctx, a.t, sa.t, b.t, sb.t, c.t, gelu=gelu)
+    torch.cuda.synchronize()
+    c.check_rest("c")
+    wbt = wb.t().contiguous()
+    ref, mag = wa @ wbt, wa.abs() @ wbt.abs()
+    tol = mag * 2.0 ** -12
+    if gelu:
+        tol = 1.13 * tol + 4e-7 * ref.abs()
+        ref = torch.special.ndtr(ref) * ref
+    bad = ~((c.t.double() - ref).abs() <= tol + 2.0 ** -8 * ref.abs())
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off"
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 1030, 400), (4090, 4104, 272)])
+def test_a_nan_scale_of_a_large_product_stays_in_its_row_or_block(ctx, m, n, k):
+    import collective_overlap_amd as cce
+    a, sa, _ = _quantised(ctx, m, k, 1, 16, uneven(m, k, m, F32))
+    b, sb, _ = _quantised(ctx, n, k, 128, 32, randn((n, k), n, 0.05))
+    want, c = (torch.empty((m, -(-n // 8) * 8), device=DEV, dtype=BF)[:, :n] for _ in range(2))
+    cce.cce_block_scaled_gemm(ctx, a.t, sa.t, b.t, sb.t, want)
+    row = torch.arange(m, device=DEV) == m // 2
+    block = (torch.arange(n, device=DEV) // 128) == 3
+    for s, i, j in ((sa, m // 2, 2), (sb, 3, 1)):
+        bytes_ = s.t.view(torch.uint8)
+        keep = bytes_[i, j].item()
+        bytes_[i, j] = 255
+        cce.cce_block_scaled_gemm(ctx, a.t, sa.t, b.t, sb.t, c)
+        bytes_[i, j] = keep
+        hit = row[:, None].expand(m, n) if s is sa else block[None].expand(m, n)
+        assert bool(torch.isnan(c[hit]).all()) and torch.equal(c[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("experts,rows,n,k", [(200, 600, 1000, 203), (70, 150, 5000, 64), (1000, 3000, 264, 40)])
+@pytest.mark.parametrize("ot", [BF, F32])
+def test_few_rows_of_many_experts(ctx, experts, rows, n, k, ot):
+    """More than 64 experts and more tiles than workgroups, uneven experts, empty ones, rows of no
+    expert: integers, so every sum is exact.  What lies behind a row of a and b is NaN."""
+    import collective_overlap_amd as cce
+    g = torch.Generator().manual_seed(experts)
+    a = Padded(rows, k, BF, 8, value=torch.randint(-3, 4, (rows, k), generator=g).float())
+    b = torch.full((experts, n, -(-k // 8) * 8 + 8), float("nan"), device=DEV, dtype=BF)[:, :, :k]
+    b.copy_(torch.randint(-3, 4, (experts, n, k), generator=g).float())
+    off = torch.randint(2, rows - 3, (experts + 1,), generator=g).sort().values
+    off[5:9] = off[9]
+    c = Padded(rows, n, ot, 8, value=torch.full((rows, n), 5.0))
+    cce.cce_ragged_gemm(ctx, a.t, b, off.to(DEV), c.t)
+    torch.cuda.synchronize()
+    c.check_rest("c")
+    want = torch.full((rows, n), 5.0, device=DEV)
+    for e in range(experts):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if hi > lo:
+            want[lo:hi] = (a.t[lo:hi].double() @ b[e].double().t().contiguous()).float()
+    assert torch.equal(c.t, want.to(ot))
