@@ -26,7 +26,9 @@ constexpr int kScaleCols = 128;   // columns that share a scale
 __device__ __forceinline__ bool before(uint32_t j, int n) { return j < static_cast<uint32_t>(n); }
 
 // Columns [j, j + 8) of a row at `base` (16-byte aligned with j a multiple of
-// 8); columns from n on read as zero.  NT: streamed past the caches.
+// 8); columns from n on read as zero.  NT: streamed past the caches.  (bf16 is
+// widened inside the check of the row's end, so the compiled code waits there
+// for each load: several in a row do not overlap within a wave, as fp32 ones do.)
 template <typename T, bool NT = false>
 __device__ __forceinline__ void load8(const T* base, uint32_t j, int n, float (&v)[8]) {
   if (before(j + 7, n)) {

@@ -356,8 +356,10 @@ __global__ __launch_bounds__(256, 1) void gemm8_kernel(G8Args a) {
 // bf16 between LDS and the matrix cores (v_mfma_f32_32x32x16_bf16), the scale
 // with it.  BM x BN x 128 tiles in the LDS layout of gemm8_kernel, NS stages:
 // the loads of tile kt + NS - 1 go out behind the barrier of tile kt, into the
-// buffer that every wave has left.  A lane's 16-byte chunk feeds two
-// instructions (the order of the k among them is the same for both operands).
+// buffer that every wave has left.  (The barrier as compiled waits for all loads
+// in flight, not for those of the tile alone: they have one tile's time.)  A
+// lane's 16-byte chunk feeds two instructions (the order of the k among them is
+// the same for both operands).
 // ---------------------------------------------------------------------------
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {

@@ -8,7 +8,8 @@
 //
 // The norm is that of the rounded r, the tensor the next layer adds to and
 // the backward pass reads, so that the gradients are those of the values in
-// memory.  Every sum is in fp32; r, y and dx are rounded once, on their store.
+// memory.  Every sum is in fp32 or more; r, y and dx are rounded once, on their
+// store.
 
 #include <hip/hip_runtime.h>
 
@@ -234,8 +235,9 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(NArgs a) {
 }
 
 // Narrow rows (per-head norms): TPR threads to a row, one vector each, so that
-// a wave takes 64 / TPR rows, and kRowsOfThread rows of a thread in flight
-// together (400000 x 128 bf16: 37 us, 5.5 TB/s; a wave per row took 109).
+// a wave takes 64 / TPR rows, and a thread kRowsOfThread of them (400000 x 128
+// bf16: 37 us, 5.5 TB/s; a wave per row took 109).  Their loads overlap in fp32;
+// in bf16 (load8) other waves' work covers them.
 constexpr int kRowsOfThread = 2;
 
 // Sum over groups of TPR lanes, in fp64.
@@ -330,7 +332,7 @@ struct BArgs {
 // adds the lines in their order.  Where the sum of squares passes fp32's range,
 // 1 / root is 0 and so is n, but the sum of w dy x may pass it too: 0 times that
 // is no mean, so the sum of w dy n is formed as it stands (0, or NaN where x is
-// infinite).  Bound by HBM: 8192 x 12288 bf16 146 us, 5.5
+// infinite).  Bound by HBM: 8192 x 12288 bf16 142 us, 5.7
 // TB/s (two passes and a third for dw: 267; without the loads ahead: 171).
 template <typename TX, typename TW, int THREADS, int RPW, int NV>
 __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
@@ -447,8 +449,9 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(BArgs a) {
 }
 
 // Narrow rows: as rmsnorm_narrow_kernel; the workgroup's rows join their sums of
-// dw through LDS, in order, to one line (400000 x 128 bf16: 60 us, 5.1 TB/s; a
-// wave per row took 252).
+// dw through LDS, in order, to one line (400000 x 128 bf16: 61 us, 5.1 TB/s; a
+// wave per row took 252).  The next row is loaded ahead of this one's sums: in
+// fp32 the loads are in flight during them, in bf16 they are waited for at once.
 template <typename TX, typename TW, int TPR>
 __global__ __launch_bounds__(kThreads) void rmsnorm_backward_narrow_kernel(BArgs a) {
   constexpr int RPW = kThreads / TPR;
@@ -631,8 +634,8 @@ struct QArgs {
 };
 
 // Blocks of 1 x 128: 16 lanes per block.  TPR threads side by side take 8 TPR
-// columns of kRowsEach rows, all of whose loads are in flight together: one
-// pass, bound by HBM (8192 x 6144 bf16: 26 us, 5.8 TB/s).
+// columns of kRowsEach rows in one pass, bound by HBM (8192 x 6144 bf16: 26 us,
+// 5.8 TB/s).  A thread's loads overlap in fp32 only (load8).
 constexpr int kRowsEach = 2;
 template <typename TX, int TPR>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QArgs a) {

@@ -502,10 +502,10 @@ __global__ __launch_bounds__(64 * kNW, 1) void ragged_kernel(RArgs a) {
   }
 }
 
-// Small products: BM x BN tiles with NS stages, so that more tiles are in
-// flight and a tile of l waits less for its loads: those of the tile NS - 1
-// further go out behind a tile's barrier, into the buffer that every wave has
-// left.  With few tiles and a long l, G groups of 4 waves each take every G-th
+// Small products: BM x BN tiles with NS stages, more workgroups per compute
+// unit: the loads of the tile NS - 1 further go out behind a tile's barrier, into
+// the buffer that every wave has left.  (The barrier as compiled waits for all
+// loads in flight, so they have one tile's time.)  With few tiles and a long l, G groups of 4 waves each take every G-th
 // tile of l with stages of their own, and join their sums through LDS in the
 // order of the groups.
 template <int N>
