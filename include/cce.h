@@ -579,8 +579,8 @@ cce_status cce_quantize_blocks(cce_ctx* ctx, cce_dtype x_t, const void* x, cce_m
  * The scales of a and b act together: one that is large beside one that is
  * small does no harm.  Products of blocks whose two factors together are below
  * 2^-117 are within 2^-109 (2^-91 beside rows with a factor above 2^119).
- * GELU of an fp32 sum x is rounded to bf16 as the other entry points round it,
- * and as fp32 result within (1.2 x^2 + 20) 2^-24 of its value.
+ * GELU of a sum x is computed as the other entry points do where the result is
+ * bf16; an fp32 result is within (1.2 x^2 + 20) 2^-24 of its value.
  * ---------------------------------------------------------------------- */
 cce_status cce_block_scaled_gemm(cce_ctx* ctx, cce_dtype out_t, const uint8_t* a, cce_mat a_shape,
                                  const uint8_t* a_scales, int64_t ld_a_scales, const uint8_t* b,

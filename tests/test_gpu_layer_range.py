@@ -338,3 +338,22 @@ def test_few_rows_of_many_experts(ctx, experts, rows, n, k, ot):
         if hi > lo:
             want[lo:hi] = (a.t[lo:hi].double() @ b[e].double().t().contiguous()).float()
     assert torch.equal(c.t, want.to(ot))
+
+
+def test_a_temporary_workspace_for_a_stream_given_as_a_handle(ctx):
+    """A stream as torch gives it, its handle, and the default stream's (0), from another current one."""
+    import collective_overlap_amd as cce
+    x, d = randn((500, 2048), 1, 1, BF).to(DEV), randn((500, 2048), 2, 1, BF).to(DEV)
+    w, dx = torch.ones(2048, device=DEV), torch.empty_like(x)
+    want = torch.empty(2048, device=DEV)
+    cce.cce_rmsnorm_backward(ctx, x, w, d, dx, want, EPS)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        got = [torch.zeros(2048, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        for g, s in zip(got, (side, side.cuda_stream, 0, None)):
+            cce.cce_rmsnorm_backward(ctx, x, w, d, dx, g, EPS, stream=s)
+            torch.cuda.synchronize()
+            assert torch.cuda.current_stream() == other
+    assert all(torch.equal(g, want) for g in got)
